@@ -83,6 +83,7 @@ typedef enum pa_dtype {
 #define PA_DEV_BAD_BLOCK 0x2     /* a block-table entry read is outside [0, nb) */
 #define PA_DEV_BAD_CONTEXT 0x4   /* context_lens[b] < 0 or > max_blocks * bs */
 #define PA_DEV_WAIT_TIMEOUT 0x8  /* a bounded wait for an async copy ran out */
+#define PA_DEV_BAD_POSITION 0x10 /* a position is outside [0, max_position) */
 
 /*
  * pa_reshape_and_cache -- store each new token's K and V into its slot.
@@ -381,6 +382,162 @@ pa_status pa_decode_attention_static(void *out, const void *query, const void *k
                                      int num_kv_heads, int head_dim, int block_size,
                                      int64_t num_blocks, float scale, pa_dtype dtype,
                                      int32_t *dev_status, void *stream);
+
+/*
+ * pa_rope_and_cache -- rotate queries and keys by their positions and store
+ * each new token's K and V into its slot: the rotary embedding and
+ * pa_reshape_and_cache in one pass over the projections' output.
+ *
+ * With r = rot_dim, token t at position p = positions[t] and a pair
+ * i < r / 2 of elements (a, b) of a query or key head,
+ *     (a, b) -> (a c - b s, b c + a s),
+ *     c = cos_sin[p][i],  s = cos_sin[p][r / 2 + i];
+ * pairs are elements (i, i + r / 2), or (2 i, 2 i + 1) with `interleaved`.
+ * Elements r .. d - 1 and all of `value` are copied bit by bit.  Arithmetic:
+ * fp32, every product and sum rounded once, the result rounded once to the
+ * element type.
+ *   query_out      device, [num_tokens, Hq, d], written for every token (also
+ *                  for padding); may be `query` itself (same stride), and must
+ *                  not overlap it otherwise.
+ *   query, key, value
+ *                  device, [num_tokens, heads, d]; heads are dense, tokens
+ *                  *_stride elements apart (a multiple of 16 bytes, at least
+ *                  heads * d), so slices of one fused projection need no copy.
+ *   num_q_heads    may be 0: no queries (query and query_out unused).
+ *   positions      device, [num_tokens] int64.
+ *   cos_sin        device, [max_position, rot_dim] fp32, 16-byte aligned.
+ *   rot_dim        a multiple of 16, at most d; 0 rotates nothing (positions
+ *                  and cos_sin unused).
+ *   slot_mapping, pools, dtypes, sizes: as in pa_reshape_and_cache.
+ * A position outside [0, max_position) sets PA_DEV_BAD_POSITION: the token's
+ * query_out row is zeros and nothing of it is cached.  Unlike
+ * pa_reshape_and_cache a call may store several tokens of a sequence before a
+ * decode: this kernel does not let the next one start early.
+ */
+pa_status pa_rope_and_cache(void *query_out, int64_t query_out_stride, const void *query,
+                            int64_t query_stride, const void *key, int64_t key_stride,
+                            const void *value, int64_t value_stride, void *k_pool, void *v_pool,
+                            const int64_t *slot_mapping, const int64_t *positions,
+                            const float *cos_sin, int rot_dim, int64_t max_position,
+                            int interleaved, int num_tokens, int num_q_heads, int num_kv_heads,
+                            int head_dim, int block_size, int64_t num_blocks, pa_dtype dtype,
+                            int32_t *dev_status, void *stream);
+
+/*
+ * Block-scaled FP8 cache.  Pools are [nb, bs, Hkv, d] bytes of E4M3 codes as
+ * for the per-tensor FP8 cache, with one fp32 scale for each block and KV head
+ * of each pool, k_scales and v_scales [nb, Hkv]:
+ *     K = code * k_scales[block][head],  V = code * v_scales[block][head].
+ * A head or a stretch of tokens with small values keeps the format's whole
+ * precision next to one with large values.  Queries, new keys and values, and
+ * outputs are bf16.  Supported: d 128 or 256, blocks of 16 or 32 tokens,
+ * Hq / Hkv in {1, 2, 4, 8}.  The pools' owner copies blocks with
+ * pa_copy_blocks_q8, which takes the scales along.
+ *
+ * pa_rope_and_cache_q8 -- append a chunk of new tokens per sequence (one for a
+ * decode step), rotated as by pa_rope_and_cache, and settle the scales.
+ *
+ * Sequence b's new tokens are rows cu_q_lens[b] .. cu_q_lens[b + 1] - 1 (n_b
+ * rows, possibly none) of query, key and value; context_lens[b] counts its
+ * cached tokens including them, so row j is stored at position
+ * ctx_b - n_b + j, in the block its table names.  For each block and head
+ * that receives rows, per pool:
+ *   w = the smallest power of two with |x| <= 448 w for every finite element x
+ *       of the new rows (exponents -64 .. 120; 2^-64 if they are all zero);
+ *   if the block's row 0 is among the new rows, the scale becomes w (what a
+ *       freed block held before does not matter); otherwise it becomes
+ *       max(scale, w), and if that raises it, the rows before the new ones are
+ *       requantised: code -> E4M3(code * old / new), exact for power-of-two
+ *       scales except where it falls below the smallest normal code;
+ *   the new rows become E4M3(x / scale), nearest, ties to even, infinities to
+ *       +-448, NaN to NaN.
+ * Rows of the block behind the new ones keep their bytes.  Keys are quantised
+ * from the fp32 results of the rotation.
+ *   query, query_out, key, value, strides, positions, cos_sin, rot_dim,
+ *                  max_position, interleaved: as in pa_rope_and_cache, bf16,
+ *                  with total_q rows.  Rows at or past cu_q_lens[num_seqs] are
+ *                  not touched.
+ *   cu_q_lens      device, [num_seqs + 1] int32, non-decreasing from 0.
+ *   max_q_len      host, >= every n_b.
+ *   block_tables, context_lens: as in pa_decode_attention; entries of blocks
+ *                  that receive no rows are not read.
+ * A sequence with n_b > max_q_len, n_b > ctx_b, ctx_b beyond its table or rows
+ * outside [0, total_q) sets PA_DEV_BAD_CONTEXT and caches nothing; an invalid
+ * block id sets PA_DEV_BAD_BLOCK and its rows are not cached; a position
+ * outside [0, max_position) sets PA_DEV_BAD_POSITION: that token is not cached
+ * and its query_out row is zeros.  Two sequences must not append to the same
+ * block in one call.
+ * The kernel lets the next one on the stream start early; it writes none of
+ * the arrays that pa_decode_attention reads before it waits, so long as the
+ * pools are not also given to that call or to pa_decode_attention_fp8.
+ */
+pa_status pa_rope_and_cache_q8(void *query_out, int64_t query_out_stride, const void *query,
+                               int64_t query_stride, const void *key, int64_t key_stride,
+                               const void *value, int64_t value_stride, void *k_pool, void *v_pool,
+                               float *k_scales, float *v_scales, const int32_t *cu_q_lens,
+                               int total_q, int max_q_len, const int32_t *block_tables,
+                               int max_blocks_per_seq, const int32_t *context_lens, int num_seqs,
+                               const int64_t *positions, const float *cos_sin, int rot_dim,
+                               int64_t max_position, int interleaved, int num_q_heads,
+                               int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                               int32_t *dev_status, void *stream);
+
+/*
+ * pa_decode_attention_q8 -- pa_decode_attention over a block-scaled FP8 cache:
+ * its definition with K and V replaced by code * scale.  query and out are
+ * bf16 [B, Hq, d]; k_scales and v_scales device [nb, Hkv] fp32, positive and
+ * finite; up to 32768 sequences; other arguments, the workspace and the errors
+ * as in pa_decode_attention (pa_decode_workspace_bytes sizes the workspace;
+ * without it each sequence is processed by one CTA per group of KV heads).
+ * Arithmetic: both tile products on E4M3 tensor cores with the codes as stored
+ * and fp32 accumulation; query rows and softmax weights are each carried as
+ * two E4M3 parts, as in pa_decode_attention_fp8.  A weight includes its
+ * block's V scale before it is split, and the running reference of the
+ * weights is the largest weight so scaled (rescaled once it grows by 2^4), so
+ * that its error is relative to what contributes most to the output; the row
+ * sums use the fp32 weights.  Nothing is read of pools, scales or query before
+ * the kernel ahead on the stream has completed.
+ */
+pa_status pa_decode_attention_q8(void *out, const void *query, const void *k_pool,
+                                 const void *v_pool, const float *k_scales, const float *v_scales,
+                                 const int32_t *block_tables, int max_blocks_per_seq,
+                                 const int32_t *context_lens, int num_seqs, int max_context_len,
+                                 int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                 int64_t num_blocks, float scale, void *workspace,
+                                 size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * pa_prefill_attention_q8 -- pa_prefill_attention over a block-scaled FP8
+ * cache: its definition with K and V replaced by code * scale (also for a few
+ * drafted tokens per sequence).  Arguments and errors as there, with k_scales
+ * and v_scales as in pa_decode_attention_q8; arithmetic as there too.
+ */
+pa_status pa_prefill_attention_q8(void *out, const void *query, const int32_t *cu_q_lens,
+                                  int total_q, int max_q_len, const void *k_pool,
+                                  const void *v_pool, const float *k_scales,
+                                  const float *v_scales, const int32_t *block_tables,
+                                  int max_blocks_per_seq, const int32_t *context_lens,
+                                  int num_seqs, int max_context_len, int num_q_heads,
+                                  int num_kv_heads, int head_dim, int block_size,
+                                  int64_t num_blocks, float scale, int32_t *dev_status,
+                                  void *stream);
+
+/*
+ * pa_copy_blocks_q8 -- pa_copy_blocks and pa_swap_blocks for a block-scaled
+ * cache: for every pair i, block block_mapping[2i + 1] of the destination
+ * pools and its scales become bit-exact copies of block block_mapping[2i] of
+ * the source pools and its scales.  The destination may be the source (a copy
+ * inside one pair of pools: destinations must not be the source of another
+ * pair); either side may be pinned host memory mapped into the device's
+ * address space.  Destinations must be distinct.  Other errors as in
+ * pa_swap_blocks.
+ */
+pa_status pa_copy_blocks_q8(void *dst_k_pool, void *dst_v_pool, float *dst_k_scales,
+                            float *dst_v_scales, int64_t dst_num_blocks, const void *src_k_pool,
+                            const void *src_v_pool, const float *src_k_scales,
+                            const float *src_v_scales, int64_t src_num_blocks,
+                            const int64_t *block_mapping, int num_pairs, int block_size,
+                            int num_kv_heads, int head_dim, int32_t *dev_status, void *stream);
 
 /* Static description of a status code. */
 const char *pa_status_string(pa_status status);

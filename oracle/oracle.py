@@ -486,3 +486,106 @@ def paged_attention_fp8_np(q, k_pool, v_pool, block_tables, context_lens, scale:
 
 __all__ += ["E4M3_MAX", "e4m3_to_f64", "f32_to_e4m3", "quantize_e4m3", "dequantize_e4m3",
             "reshape_and_cache_fp8_np", "paged_attention_fp8_np"]
+
+
+# --------------------------------------------------------------------------
+# Rotary embedding and the block-scaled E4M3 cache (numpy)
+#
+# The pages hold a cache of rotated keys and name quantised caches, but fix
+# neither formula.  Readings: a pair (a, b) of a head's first rot_dim elements
+# at position p becomes (a c - b s, b c + a s) with c = table[p][i] and
+# s = table[p][rot_dim / 2 + i]; pairs are (i, i + rot_dim / 2), or
+# (2 i, 2 i + 1) when interleaved; binary32, each product and sum rounded
+# once.  A block-scaled cache holds E4M3 codes with one binary32 scale per
+# (block, KV head) and pool.
+# --------------------------------------------------------------------------
+
+def f32_to_bf16_raw(x) -> np.ndarray:
+    """bf16 bit patterns (uint16) of binary32 values, to nearest even."""
+    x = np.ascontiguousarray(x, dtype=np.float32)
+    u = x.view(np.uint32).astype(np.uint64)
+    r = ((u + 0x7FFF + ((u >> 16) & 1)) >> 16).astype(np.uint16)
+    return np.where(np.isnan(x), np.uint16(0x7FFF), r)
+
+
+def rotate_f32(x, positions, table, rot_dim: int, interleaved: bool) -> np.ndarray:
+    """x [T, H, d] binary32 with its first rot_dim elements rotated."""
+    x = np.asarray(x, dtype=np.float32)
+    y = x.copy()
+    if rot_dim == 0:
+        return y
+    half = rot_dim // 2
+    i = np.arange(half)
+    ia, ib = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+    row = np.asarray(table, dtype=np.float32)[np.asarray(positions, dtype=np.int64)]
+    c, s = row[:, None, :half], row[:, None, half:]
+    a, b = x[..., ia], x[..., ib]
+    with np.errstate(invalid="ignore", over="ignore"):
+        y[..., ia] = a * c - b * s
+        y[..., ib] = b * c + a * s
+    return y
+
+
+def block_scale(amax) -> np.float32:
+    """The smallest power of two w, 2^-64 <= w <= 2^120, with amax <= 448 w."""
+    w = 2.0 ** -64
+    while float(amax) > 448.0 * w and w < 2.0 ** 120:
+        w *= 2.0
+    return np.float32(w)
+
+
+def append_q8_np(pool, scales, x, cu_q_lens, block_tables, context_lens):
+    """Appends the rows x [total, Hkv, d] (binary32) of each sequence's chunk
+    to block-scaled pools: uint8 codes [nb, bs, Hkv, d], scales [nb, Hkv].
+    Returns new arrays.  Sequence b's rows cu[b] .. cu[b + 1] - 1 end at
+    position context_lens[b] - 1."""
+    pool = np.array(pool, dtype=np.uint8, copy=True)
+    scales = np.array(scales, dtype=np.float32, copy=True)
+    x = np.asarray(x, dtype=np.float32)
+    bs, hkv = pool.shape[1], pool.shape[2]
+    for b in range(len(context_lens)):
+        q0, n, ctx = int(cu_q_lens[b]), int(cu_q_lens[b + 1] - cu_q_lens[b]), int(context_lens[b])
+        t = 0
+        while t < n:
+            pos = ctx - n + t
+            r0 = pos % bs
+            rows = min(bs - r0, n - t)
+            blk = int(block_tables[b][pos // bs])
+            for h in range(hkv):
+                new = x[q0 + t:q0 + t + rows, h]
+                fin = np.abs(new[np.isfinite(new)])
+                w = block_scale(fin.max() if fin.size else 0.0)
+                old = scales[blk, h]
+                s = w if r0 == 0 else np.maximum(old, w)
+                if r0 > 0 and s != old:
+                    held = e4m3_to_f64(pool[blk, :r0, h]).astype(np.float32)
+                    pool[blk, :r0, h] = f32_to_e4m3(held * (np.float32(old) / np.float32(s)))
+                pool[blk, r0:r0 + rows, h] = quantize_e4m3(new, s)
+                scales[blk, h] = s
+            t += rows
+    return pool, scales
+
+
+def dequantize_q8(pool, scales) -> np.ndarray:
+    """fp64 values code * scale[block, head] (exact)."""
+    return e4m3_to_f64(pool) * np.asarray(scales, dtype=np.float32).astype(np.float64)[:, None, :, None]
+
+
+def paged_attention_q8_np(q, k_pool, v_pool, k_scales, v_scales, block_tables, context_lens,
+                          scale: float) -> np.ndarray:
+    """Exact fp64 decode attention over a block-scaled cache (raw bf16 query)."""
+    return paged_attention_np(to_f64(q, "bf16"), dequantize_q8(k_pool, k_scales),
+                              dequantize_q8(v_pool, v_scales), block_tables, context_lens, scale,
+                              "f64")
+
+
+def prefill_attention_q8_np(q, k_pool, v_pool, k_scales, v_scales, block_tables, context_lens,
+                            cu_q_lens, scale: float) -> np.ndarray:
+    """Exact fp64 causal chunk attention over a block-scaled cache."""
+    return prefill_attention_np(to_f64(q, "bf16"), dequantize_q8(k_pool, k_scales),
+                                dequantize_q8(v_pool, v_scales), block_tables, context_lens,
+                                cu_q_lens, scale, "f64")
+
+
+__all__ += ["f32_to_bf16_raw", "rotate_f32", "block_scale", "append_q8_np", "dequantize_q8",
+            "paged_attention_q8_np", "prefill_attention_q8_np"]

@@ -24,6 +24,7 @@
 
 #include "pa.h"
 #include "pa_testing.h"
+#include "pa_host.cuh"
 #include "pa_launch.cuh"
 #include "pa_prefill.cuh"
 
@@ -44,7 +45,7 @@ std::atomic<int> g_test_withhold{-1};
 // to 256 SMs).
 constexpr int kWorkspaceCtas = 256;
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using pa::aligned16;
 
 int ilog2_exact(int v)
 {
@@ -214,19 +215,7 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(const CopyParams p, in
         to[c] = __ldcg(from + c);
 }
 
-// True if the GPU can read and write `ptr` at that same address: device
-// memory, or pinned host memory mapped into the unified address space.
-bool device_addressable(const void *ptr)
-{
-    cudaPointerAttributes a;
-    if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
-        cudaGetLastError();   // clear the error of an unknown pointer
-        return false;
-    }
-    if (a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged)
-        return true;
-    return a.type == cudaMemoryTypeHost && a.devicePointer == ptr;
-}
+using pa::device_addressable;
 
 pa_status launch_copy(CopyParams &p, int block_size, int num_kv_heads, int head_dim,
                       pa_dtype dtype, void *stream)
@@ -659,6 +648,65 @@ pa_status stream_k_need(size_t *need, const void *out, const void *query, const 
 
 }  // namespace
 
+// Services of pa_host.cuh.
+namespace pa {
+
+void count_launch() { ++g_launches; }
+
+unsigned long long test_wait_ns() { return g_test_wait_ns.load(); }
+
+int test_withhold_cta() { return g_test_withhold.load(); }
+
+// True if the GPU can read and write `ptr` at that same address: device
+// memory, or pinned host memory mapped into the unified address space.
+bool device_addressable(const void *ptr)
+{
+    cudaPointerAttributes a;
+    if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
+        cudaGetLastError();   // clear the error of an unknown pointer
+        return false;
+    }
+    if (a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged)
+        return true;
+    return a.type == cudaMemoryTypeHost && a.devicePointer == ptr;
+}
+
+pa_status check_attention(const void *out, const void *query, const void *k_pool,
+                          const void *v_pool, const int32_t *block_tables, int max_blocks,
+                          const int32_t *context_lens, int num_seqs, int max_context_len,
+                          int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                          int64_t num_blocks, pa_dtype dtype, int *group, int *bs_log2)
+{
+    return check_attention_args(out, query, k_pool, v_pool, block_tables, max_blocks,
+                                context_lens, num_seqs, max_context_len, num_q_heads,
+                                num_kv_heads, head_dim, block_size, num_blocks, dtype, group,
+                                bs_log2);
+}
+
+bool pool_map_grouped(CUtensorMap *out, const void *base, int64_t nb, int bs, int hkv, int d,
+                      pa_dtype dt, int tr)
+{
+    return encode_pool_map(out, base, nb, bs, hkv, d, dt, tr, 1, true);
+}
+
+bool query_map(CUtensorMap *out, const void *query, int total_q, int hq, int d, int group,
+               int tokens)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc)
+        return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)hq, (cuuint64_t)total_q};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)hq * d * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(query), dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace pa
+
 extern "C" {
 
 const char *pa_status_string(pa_status status)
@@ -912,20 +960,8 @@ pa_status pa_prefill_attention(void *out, const void *query, const int32_t *cu_q
         // 5th-generation tensor cores: the query rows of the CTA come by TMA
         // through a 3-D map over [total_q, Hq, d] (box: 64 elements, the
         // group's heads, the CTA's tokens)
-        EncodeTiledFn enc = encode_fn();
-        if (!enc)
-            return PA_ERR_CUDA;
         alignas(64) CUtensorMap qmap;
-        const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)num_q_heads,
-                                    (cuuint64_t)total_q};
-        const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2,
-                                       (cuuint64_t)num_q_heads * head_dim * 2};
-        const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tq};
-        const cuuint32_t estr[3] = {1, 1, 1};
-        if (enc(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(query), dims, strides,
-                box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        if (!pa::query_map(&qmap, query, total_q, num_q_heads, head_dim, group, tq))
             return PA_ERR_CUDA;
         st = pa::prefill_tc_dispatch(head_dim, group, qmap, tk, tv, p, (int)grid,
                                      static_cast<cudaStream_t>(stream));

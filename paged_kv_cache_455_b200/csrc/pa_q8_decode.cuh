@@ -1,0 +1,1041 @@
+// pa_q8_decode.cuh -- decode attention over a block-scaled E4M3 cache on the
+// 5th-generation tensor cores (tcgen05.mma kind::f8f6f4, accumulators in
+// tensor memory).
+//
+//   s_t = scale ks(t) (q . K_t),   o = sum_t p_t vs(t) V_t / sum_t p_t,
+// p_t = exp(s_t - max s), K_t and V_t the codes of token t, ks(t) and vs(t)
+// the scales of its block.
+//
+// Tile.  128 rows of K and of V: hpc KV heads (the largest of 4, 2, 1 that
+// divides Hkv) times 128 / hpc consecutive tokens of one sequence, so a CTA
+// reads whole token rows of its head group.  Rows 32 w .. 32 w + 31 belong to
+// softmax warp w: 32 tokens of head w / (4 / hpc).  Both products take the
+// cache as the A operand, straight from the stage the TMA filled:
+//   S   [128 rows x NQ]  = K (K-major, 128 x d) * Q^T, NQ = the group's query
+//       rows, each as two E4M3 parts; a row uses only its own head's columns
+//       (the tensor cores have room: 128 x NQ x d per 2 * 128 * d bytes)
+//   O^T [128 d x NP] += V_w^T (MN-major, 128 d x 32 tokens) * P_w, for each
+//       warp w and half of d; P_w holds the warp's weights as three E5M2 parts
+// so no code is ever converted or moved by a thread, and the softmax of one
+// tile is 32 tokens per warp, one per lane.
+//
+// Weights.  x_t = 2^11 vs(t) 2^(s_t - m) with m a running reference per head
+// and warp, at least max_t (s_t + log2 vs(t)) - 4 (log2 units): x_t <= 2^15.
+// The three E5M2 parts are the value rounded to 3 bits, the rest rounded to
+// 3, and again: error 2^-9 of x_t down to x_t = 2^-8 and 2^-17 below, that is
+// 2^-28 of the largest weight, so that many small weights next to a large one
+// are not lost.  The row sums take the fp32 weights 2^(s_t - m).  Because m
+// follows the weights with their scales, the errors are relative to what the
+// output is made of, whatever the scales' spread.
+//
+// Warps: 0-3 softmax and epilogue, 4 MMA issue, 5 TMA and block scales, 6-7
+// query rows.  Work is split as in decode_kernel: every CTA owns an equal,
+// contiguous range of the batch's tiles (mode 0), or whole segments (mode 1);
+// a segment is the run of tiles of one sequence and head group.  The pieces
+// of a segment cut by range borders go to the workspace as fp32 (maximum, sum,
+// accumulator), and q8_merge_kernel joins them after this kernel.
+#pragma once
+
+#include "pa_kernels.cuh"
+#include "pa_ptx8.cuh"
+
+namespace pa {
+
+constexpr int kQ8Threads = 256;
+constexpr int kQ8Tile = 128;              // rows of K and V per tile (MMA M)
+constexpr int kQ8SmemStages = 6 * 32768;  // bytes of the stage ring
+constexpr float kQ8Grow = 4.f;            // log2 growth that makes a rescale
+constexpr float kQ8Weight = 2048.f;       // 2^11: a weight at the reference
+
+struct Q8DecodeParams {
+    __nv_bfloat16 *out;
+    const __nv_bfloat16 *q;
+    const float *k_scales, *v_scales;
+    const int32_t *block_tables, *context_lens;
+    float *pieces;           // mode 0: two slots per CTA
+    int4 *cuts;              // mode 0: per CTA (sequence, head group, pieces or 0, -)
+    int32_t *dev_status;
+    int64_t num_blocks;
+    int num_seqs, num_q_heads, num_kv_heads;
+    int max_blocks, block_size, bs_log2;
+    int ctx_cap;
+    int hpc, hpc_log2;       // KV heads per tile
+    int tt_log2;             // tokens per tile = 128 / hpc
+    int head_groups;
+    int mode;                // 0: equal ranges, 1: whole segments
+    int slot_floats;
+    float scale_log2;
+    uint64_t wait_ns;
+    int withhold_cta;        // test hook, as in DecodeParams
+};
+
+// Per-stage metadata, written by the TMA warp with the stage.
+struct Q8Meta {
+    int b, hg, j, ns;        // sequence, head group, tile in the segment, its tiles
+    int n;                   // valid tokens of the tile
+    int first, last;         // first / last tile of the segment in this CTA's range
+    int bad;                 // an invalid block id
+    float ks[8], vs[8];      // scales of the tile's 16-row boxes
+};
+
+template <int D, int G>
+struct Q8Smem {
+    static constexpr int kStage = 2 * kQ8Tile * D;
+    static constexpr int kStages = kQ8SmemStages / kStage;           // 3 (d 256), 6 (d 128)
+    static constexpr int kQRows = 8 * G < 16 ? 16 : 8 * G;           // up to 4 heads, 2 parts
+    static constexpr int kQBufs = (D == 256 && G == 8) ? 1 : 2;
+    static constexpr int GP = G <= 4 ? 4 : 8;                        // rows of one weight part
+    static constexpr int NP = 4 * GP;                                // 3 parts, padded
+    static constexpr int kP = NP * 32;                               // bytes of a warp's weights
+    static constexpr int q_off = kQ8SmemStages;
+    static constexpr int p_off = q_off + kQBufs * kQRows * D;
+    static constexpr int meta_off = p_off + 2 * 4 * kP;
+    static constexpr int sf_off = meta_off + kStages * (int)sizeof(Q8Meta);
+    static constexpr int stat_off = sf_off + kQBufs * 4 * G * 4;     // m, l per warp and head
+    static constexpr int alpha_off = stat_off + 4 * 2 * G * 4;
+    static constexpr int bar_off = (alpha_off + 2 * 4 * G * 4 + 15) / 16 * 16;
+    static constexpr int kBars = 3 * kStages + 8 + 2 * kQBufs + 1;
+    static constexpr int flag_off = bar_off + 8 * kBars;
+    static constexpr int cbase_off = flag_off + 16;
+    static constexpr int bytes = 1024 + cbase_off + 4 * (kMaxChunks + 1);
+    static_assert(bytes <= kSmemBudget, "shared memory per CTA");
+    // tensor memory columns: two S buffers of 64, then the accumulators
+    static constexpr int o_cols = 4 * (D / 128) * NP;
+    static constexpr uint32_t tmem_cols = 128 + o_cols <= 256 ? 256u : 512u;
+};
+
+// Position in the batch's sequence of segments (whole warp, uniform).
+struct Q8Walk {
+    int b, hg;       // sequence, head group
+    int ctx, nt;     // its effective length, tiles of the segment
+    int g0;          // global index of the segment's first tile
+};
+
+__device__ __forceinline__ int q8_tiles(int ctx, const Q8DecodeParams &p)
+{
+    return (ctx + (1 << p.tt_log2) - 1) >> p.tt_log2;
+}
+
+// cbase[c] = global index of the first tile of sequence 32 c; returns the
+// total.  Every thread of the CTA.
+__device__ __forceinline__ int q8_prefix(const Q8DecodeParams &p, int *cbase)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
+    const int nch = (p.num_seqs + 31) >> 5;
+    for (int c = warp; c < nch; c += nwarps) {
+        const int b = c * 32 + lane;
+        int t = b < p.num_seqs ? q8_tiles(eff_ctx(p.context_lens[b], p.ctx_cap), p) * p.head_groups
+                               : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            t += __shfl_xor_sync(kFull, t, o);
+        if (lane == 0)
+            cbase[c + 1] = t;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int carry = 0;
+        if (lane == 0)
+            cbase[0] = 0;
+        for (int c0 = 0; c0 < nch; c0 += 32) {
+            const int c = c0 + lane;
+            int v = c < nch ? cbase[c + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(kFull, v, o);
+                if (lane >= o)
+                    v += u;
+            }
+            if (c < nch)
+                cbase[c + 1] = carry + v;
+            carry += __shfl_sync(kFull, v, 31);
+        }
+    }
+    __syncthreads();
+    return cbase[nch];
+}
+
+// The segment holding tile g (below the total).
+__device__ __forceinline__ Q8Walk q8_walk_at(int g, const Q8DecodeParams &p, const int *cbase,
+                                             int lane)
+{
+    const int c = chunk_of(cbase, (p.num_seqs + 31) >> 5, g);
+    const int b = c * 32 + lane;
+    const int ctx = b < p.num_seqs ? eff_ctx(p.context_lens[b], p.ctx_cap) : 0;
+    const int nt = q8_tiles(ctx, p);
+    int incl = nt * p.head_groups;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o)
+            incl += u;
+    }
+    const unsigned past = __ballot_sync(kFull, cbase[c] + incl > g);
+    const int src = past ? __ffs(past) - 1 : 31;
+    Q8Walk w;
+    w.b = c * 32 + src;
+    w.ctx = __shfl_sync(kFull, ctx, src);
+    w.nt = max(__shfl_sync(kFull, nt, src), 1);
+    const int start = cbase[c] + __shfl_sync(kFull, incl - nt * p.head_groups, src);
+    w.hg = (g - start) / w.nt;
+    w.g0 = start + w.hg * w.nt;
+    return w;
+}
+
+// Moves to the next segment (the batch must hold one).
+__device__ __forceinline__ void q8_walk_next(Q8Walk &w, const Q8DecodeParams &p, int lane)
+{
+    w.g0 += w.nt;
+    if (++w.hg < p.head_groups)
+        return;
+    w.hg = 0;
+    for (int b0 = w.b + 1; b0 < p.num_seqs; b0 += 32) {
+        const int b = b0 + lane;
+        const int ctx = b < p.num_seqs ? eff_ctx(p.context_lens[b], p.ctx_cap) : 0;
+        const unsigned some = __ballot_sync(kFull, ctx > 0);
+        if (some) {
+            const int src = __ffs(some) - 1;
+            w.b = b0 + src;
+            w.ctx = __shfl_sync(kFull, ctx, src);
+            w.nt = q8_tiles(w.ctx, p);
+            return;
+        }
+    }
+}
+
+__device__ __forceinline__ int q8_range_begin(int x, int C, int T, const Q8DecodeParams &p,
+                                              const int *cbase, int lane)
+{
+    if (x >= C)
+        return T;
+    const int g = (int)((int64_t)x * T / C);
+    if (p.mode == 0 || g >= T)
+        return g;
+    const Q8Walk w = q8_walk_at(g, p, cbase, lane);
+    return w.g0 == g ? g : w.g0 + w.nt;
+}
+
+// x to the nearest value with three significant bits (E5M2's; x >= 0, finite).
+__device__ __forceinline__ float round3(float x)
+{
+    return __uint_as_float((__float_as_uint(x) + 0x100000u) & 0xffe00000u);
+}
+
+__device__ __forceinline__ uint32_t e5m2x2(float lo, float hi)
+{
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
+}
+
+__device__ __forceinline__ void st_shared_u8(uint32_t a, uint32_t v)
+{
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kQ8Threads, 1)
+    q8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                     const __grid_constant__ CUtensorMap tmap_v, const Q8DecodeParams p)
+{
+    using L = Q8Smem<D, G>;
+    constexpr int S = L::kStages, QB = L::kQBufs, GP = L::GP, NP = L::NP;
+    constexpr int HALVES = D / 128;
+    constexpr int GROUP = 8 * D;                 // bytes between 8-row groups
+    extern __shared__ uint8_t smem_raw[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gen = smem_raw + (base - raw);
+    Q8Meta *meta = reinterpret_cast<Q8Meta *>(gen + L::meta_off);
+    float *sf = reinterpret_cast<float *>(gen + L::sf_off);
+    float *stat = reinterpret_cast<float *>(gen + L::stat_off);
+    float *alpha_s = reinterpret_cast<float *>(gen + L::alpha_off);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + L::flag_off);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen + L::flag_off + 4);
+    int *cbase = reinterpret_cast<int *>(gen + L::cbase_off);
+    const uint32_t bars = base + L::bar_off;
+    const uint32_t kfull = bars, vfull = kfull + 8 * S, empty = vfull + 8 * S,
+                   sfull = empty + 8 * S, sfree = sfull + 16, pready = sfree + 16,
+                   pvdone = pready + 16, qfull = pvdone + 16, qempty = qfull + 8 * QB,
+                   drain = qempty + 8 * QB;
+    const int hpc = p.hpc, sub_log2 = 2 - p.hpc_log2;   // 4 / hpc warps per head
+    const int nq = max(16, 2 * G * hpc);                // columns of S
+    const int tt = 1 << p.tt_log2;
+
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            ptx::mbar_init(kfull + 8 * i, 1);
+            ptx::mbar_init(vfull + 8 * i, 1);
+            ptx::mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(sfull + 8 * i, 1);
+            ptx::mbar_init(sfree + 8 * i, 4);
+            ptx::mbar_init(pready + 8 * i, 4);
+            ptx::mbar_init(pvdone + 8 * i, 1);
+        }
+        for (int i = 0; i < QB; ++i) {
+            ptx::mbar_init(qfull + 8 * i, 2);
+            ptx::mbar_init(qempty + 8 * i, 5);   // the last S of the segment, softmax warps
+        }
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0;
+    }
+    ptx::fence_mbar_init();
+    // weight rows that no head fills stay zero
+    for (int i = tid; i < 2 * 4 * L::kP / 16; i += kQ8Threads)
+        reinterpret_cast<uint4 *>(gen + L::p_off)[i] = make_uint4(0, 0, 0, 0);
+    ptx::fence_proxy_async_smem();
+    if (warp == 4) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_holder), L::tmem_cols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    // lengths and block tables are read before the kernel ahead has completed
+    const int total = q8_prefix(p, cbase);              // contains __syncthreads
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const uint32_t o_tm = tmem + 128;
+    const int C = min((int)gridDim.x, max(total, 1));
+    const int R0 = q8_range_begin(blockIdx.x, C, total, p, cbase, lane);
+    const int R1 = q8_range_begin(blockIdx.x + 1, C, total, p, cbase, lane);
+    if (tid == 0)
+        ptx::grid_launch_dependents();
+    const uint64_t lim = p.wait_ns;
+
+    if (warp == 5) {
+        // ============================================== TMA and block scales
+        // Lane l serves box l % 8 (rows 16 (l % 8) ..: 16 tokens of one head)
+        // of tile l / 8 of a batch of four tiles; a batch's block ids are
+        // fetched one batch ahead.
+        const int box = lane & 7, slot = lane >> 3;
+        const int bw = box >> 1;                        // the box's softmax warp
+        const int bhead = bw >> sub_log2;
+        const int btok = ((bw & ((1 << sub_log2) - 1)) << 5) + ((box & 1) << 4);
+        struct Batch {
+            int b, hg, j, ns, n, id;
+            bool active;
+        };
+        bool ok = true;
+        int issued = R0;
+        if (R0 < R1) {
+            if (lane == 0) {
+                ptx::prefetch_tensormap(&tmap_k);
+                ptx::prefetch_tensormap(&tmap_v);
+            }
+            const uint64_t policy = ptx::policy_evict_first();
+            Q8Walk w = q8_walk_at(R0, p, cbase, lane);
+            auto fill = [&](int g) {
+                Batch d = {0, 0, 0, 1, 0, -1, false};
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    if (g + i >= R1)
+                        break;
+                    if (g + i >= w.g0 + w.nt)
+                        q8_walk_next(w, p, lane);
+                    if (slot == i) {
+                        d.b = w.b;
+                        d.hg = w.hg;
+                        d.j = g + i - w.g0;
+                        d.ns = w.nt;
+                        const int t0 = d.j << p.tt_log2;
+                        d.n = min(tt, w.ctx - t0);
+                        d.active = btok < d.n;
+                        if (d.active)
+                            d.id = __ldg(p.block_tables + (int64_t)w.b * p.max_blocks +
+                                         ((t0 + btok) >> p.bs_log2));
+                    }
+                }
+                return d;
+            };
+            Batch cur = fill(R0), nxt = cur;
+            // pools and scales may be written by the kernel ahead
+            ptx::grid_wait_prerequisites();
+            for (int g = R0; ok && g < R1; g += 4, cur = nxt) {
+                const bool valid = cur.active && cur.id >= 0 && (int64_t)cur.id < p.num_blocks;
+                const int head = cur.hg * hpc + bhead;
+                float ks = 0.f, vs = 0.f;
+                if (valid) {
+                    const int64_t at = (int64_t)cur.id * p.num_kv_heads + head;
+                    ks = __ldcg(p.k_scales + at);
+                    vs = __ldcg(p.v_scales + at);
+                }
+                const unsigned vmask = __ballot_sync(kFull, valid);
+                const unsigned bmask = __ballot_sync(kFull, cur.active && !valid);
+                nxt = fill(g + 4);
+                for (int i = 0; i < 4 && g + i < R1; ++i) {
+                    const int k = g + i - R0, s = k % S;
+                    if (__any_sync(kFull, *abort_flag != 0))
+                        break;
+                    if (k >= S &&
+                        !__all_sync(kFull, ptx::mbar_wait_bounded(empty + 8 * s,
+                                                                  (uint32_t)((k / S - 1) & 1),
+                                                                  lim))) {
+                        ok = false;
+                        break;
+                    }
+                    // test hook: this CTA's second tile is never copied
+                    const bool withhold = (int)blockIdx.x == p.withhold_cta && k == 1;
+                    const unsigned mine = (vmask >> (8 * i)) & 0xffu;
+                    const int from = 8 * i;
+                    const int mb = __shfl_sync(kFull, cur.b, from);
+                    const int mhg = __shfl_sync(kFull, cur.hg, from);
+                    const int mj = __shfl_sync(kFull, cur.j, from);
+                    const int mns = __shfl_sync(kFull, cur.ns, from);
+                    const int mn = __shfl_sync(kFull, cur.n, from);
+                    if (lane == 0) {
+                        Q8Meta &m = meta[s];
+                        m.b = mb;
+                        m.hg = mhg;
+                        m.j = mj;
+                        m.ns = mns;
+                        m.n = mn;
+                        m.first = mj == 0 || k == 0;
+                        m.last = mj == mns - 1 || g + i == R1 - 1;
+                        m.bad = ((bmask >> (8 * i)) & 0xffu) != 0;
+                        const uint32_t tx = (uint32_t)(__popc(mine) * 16 * D);
+                        ptx::mbar_expect_tx(kfull + 8 * s, tx);
+                        ptx::mbar_expect_tx(vfull + 8 * s, tx);
+                    }
+                    __syncwarp();
+                    if (slot == i) {
+                        if (valid && !withhold) {
+                            const int t0 = (cur.j << p.tt_log2) + btok;
+                            const int row = cur.id * p.block_size + (t0 & (p.block_size - 1));
+                            const uint32_t dst = base + (uint32_t)(s * L::kStage + box * 16 * D);
+                            ptx::tma_load_5d(dst, &tmap_k, 0, 0, 0, row >> 3, head, kfull + 8 * s,
+                                             policy);
+                            ptx::tma_load_5d(dst + kQ8Tile * D, &tmap_v, 0, 0, 0, row >> 3, head,
+                                             vfull + 8 * s, policy);
+                        }
+                        meta[s].ks[box] = ks;
+                        meta[s].vs[box] = vs;
+                    }
+                    __syncwarp();
+                    // (the arrivals release the metadata and the scales)
+                    if (lane == 0) {
+                        ptx::mbar_arrive(kfull + 8 * s);
+                        ptx::mbar_arrive(vfull + 8 * s);
+                    }
+                    issued = g + i + 1;
+                }
+                if (issued < min(g + 4, R1))
+                    break;
+            }
+        }
+        if (!ok && lane == 0) {
+            report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
+            *abort_flag = 1;
+        }
+        if (issued < R1) {
+            // given up: let the copies in flight land before the CTA ends
+            for (int k = max(0, issued - R0 - S); k < issued - R0; ++k) {
+                ptx::mbar_wait_bounded(kfull + 8 * (k % S), (uint32_t)((k / S) & 1), lim);
+                ptx::mbar_wait_bounded(vfull + 8 * (k % S), (uint32_t)((k / S) & 1), lim);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 4) {
+        // ======================================================= MMA issue
+        auto ready = [&](uint32_t bar, uint32_t parity) -> bool {
+            if (__all_sync(kFull, ptx::mbar_test_wait(bar, parity)))
+                return true;
+            if (__any_sync(kFull, *abort_flag != 0))
+                return false;
+            return __all_sync(kFull, ptx::mbar_wait_bounded(bar, parity, lim));
+        };
+        const uint32_t idesc_s = ptx::umma_idesc_f8(128, nq, false, false, false, false);
+        constexpr uint32_t idesc_o = ptx::umma_idesc_f8(128, NP, false, true, true, false);
+        bool ok = true;
+        int seg = 0;
+        int fresh_prev = 0;
+        auto issue_pv = [&](int k, int fresh) -> bool {
+            const int s = k % S;
+            if (!ready(pready + 8 * (k & 1), (uint32_t)((k >> 1) & 1)) ||
+                !ready(vfull + 8 * s, (uint32_t)((k / S) & 1)))
+                return false;
+            ptx::tc_fence_after();
+            const uint32_t vst = base + (uint32_t)(s * L::kStage + kQ8Tile * D);
+            const uint32_t pst = base + (uint32_t)(L::p_off + (k & 1) * 4 * L::kP);
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint64_t bd = ptx::umma_desc_plain(pst + w * L::kP, 128, 256);
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h)
+                        ptx::umma_f8_ss(o_tm + (uint32_t)((w * HALVES + h) * NP),
+                                        ptx::umma_desc_sw128(vst + w * 32 * D + h * 1024, 1024,
+                                                             GROUP),
+                                        bd, idesc_o, fresh == 0);
+                }
+                ptx::umma_commit(empty + 8 * s);
+                ptx::umma_commit(pvdone + 8 * (k & 1));
+            }
+            __syncwarp();
+            return true;
+        };
+        const int nk = R1 - R0;
+        for (int k = 0; k < nk; ++k) {
+            const int s = k % S;
+            if (!(ok = ready(kfull + 8 * s, (uint32_t)((k / S) & 1))))
+                break;
+            const int first = meta[s].first, last = meta[s].last;
+            const int qb = seg % QB;
+            if (first && !(ok = ready(qfull + 8 * qb, (uint32_t)((seg / QB) & 1))))
+                break;
+            if (k >= 2 && !(ok = ready(sfree + 8 * (k & 1), (uint32_t)(((k >> 1) - 1) & 1))))
+                break;
+            ptx::tc_fence_after();
+            const uint64_t ad = ptx::umma_desc_sw128(base + (uint32_t)(s * L::kStage), 16, GROUP);
+            const uint64_t bd = ptx::umma_desc_sw128(
+                base + (uint32_t)(L::q_off + qb * L::kQRows * D), 16, GROUP);
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk) {
+                    const uint64_t off = (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
+                    ptx::umma_f8_ss(tmem + (uint32_t)((k & 1) * 64), ad + off, bd + off, idesc_s,
+                                    kk > 0);
+                }
+                ptx::umma_commit(sfull + 8 * (k & 1));
+                if (last)
+                    ptx::umma_commit(qempty + 8 * qb);
+            }
+            __syncwarp();
+            seg += last;
+            if (k >= 1 && !(ok = issue_pv(k - 1, fresh_prev)))
+                break;
+            fresh_prev = first;
+        }
+        if (ok && nk > 0)
+            ok = issue_pv(nk - 1, fresh_prev);
+        if (!ok) {
+            if (lane == 0) {
+                report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // products already issued finish before the memory goes
+            if (ptx::elect_one())
+                ptx::umma_commit(drain);
+            __syncwarp();
+            ptx::mbar_wait_bounded(drain, 0, lim);
+        }
+        __syncwarp();
+    } else if (warp >= 6) {
+        // ====================================================== query rows
+        // Row (h, g) of a segment is scaled by a power of two (largest
+        // element in [128, 256)) and split into hi = e4m3(y) and
+        // lo = e4m3(y - hi), as over the per-tensor FP8 cache; they become
+        // rows (2 h) G + g and (2 h + 1) G + g of the B operand.
+        ptx::grid_wait_prerequisites();
+        bool ok = true;
+        if (R0 < R1) {
+            constexpr int E = D / 32;                    // elements per lane
+            Q8Walk w = q8_walk_at(R0, p, cbase, lane);
+            for (int seg = 0; w.g0 < R1; ++seg) {
+                const int qb = seg % QB;
+                if (__any_sync(kFull, *abort_flag != 0))
+                    break;
+                const int rows = hpc * G;
+                const __nv_bfloat16 *src = p.q + ((int64_t)w.b * p.num_q_heads +
+                                                  (int64_t)w.hg * rows) * D;
+                constexpr int RW = 4 * G / 2;            // rows per warp, at most
+                uint32_t x[RW][E / 2];
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const int r = 2 * i + (warp - 6);
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e)
+                        x[i][e] = 0;
+                    if (r < rows) {
+                        if constexpr (E == 8) {
+                            const uint4 v = __ldg(
+                                reinterpret_cast<const uint4 *>(src + (int64_t)r * D) + lane);
+                            x[i][0] = v.x;
+                            x[i][1] = v.y;
+                            x[i][2] = v.z;
+                            x[i][3] = v.w;
+                        } else {
+                            const uint2 v = __ldg(
+                                reinterpret_cast<const uint2 *>(src + (int64_t)r * D) + lane);
+                            x[i][0] = v.x;
+                            x[i][1] = v.y;
+                        }
+                    }
+                }
+                if (seg >= QB &&
+                    !__all_sync(kFull, ptx::mbar_wait_bounded(qempty + 8 * qb,
+                                                              (uint32_t)((seg / QB - 1) & 1),
+                                                              lim))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t qst = base + (uint32_t)(L::q_off + qb * L::kQRows * D);
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const int r = 2 * i + (warp - 6);
+                    if (r >= rows)
+                        continue;
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e)
+                        top = max(top, max(x[i][e] << 16 & 0x7fffffffu, x[i][e] & 0x7fff0000u));
+                    top = __reduce_max_sync(kFull, top);
+                    const int ef = (int)(top >> 23);
+                    const float sigma = __uint_as_float((uint32_t)min(254, 261 - ef) << 23);
+                    uint32_t hi[E / 4], lo[E / 4];
+#pragma unroll
+                    for (int e = 0; e < E / 4; ++e) {
+                        uint32_t h2[2], l2[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float y0 = ptx::bf16lo_to_f32(x[i][2 * e + k]) * sigma;
+                            const float y1 = ptx::bf16hi_to_f32(x[i][2 * e + k]) * sigma;
+                            h2[k] = f32x2_to_e4m3x2(y0, y1);
+                            const uint32_t f = e4m3x2_to_f16x2(h2[k]);
+                            l2[k] = f32x2_to_e4m3x2(y0 - ptx::f16lo_to_f32(f),
+                                                    y1 - ptx::f16hi_to_f32(f));
+                        }
+                        hi[e] = h2[0] | (h2[1] << 16);
+                        lo[e] = l2[0] | (l2[1] << 16);
+                    }
+                    const int h = r / G, g = r - h * G;
+                    const int byte = lane * E;           // within the row
+                    auto at = [&](int n) {
+                        return qst + (uint32_t)((n >> 3) * GROUP + (byte >> 7) * 1024 + (n & 7) * 128 +
+                                                ((((byte & 127) >> 4) ^ (n & 7)) << 4) + (byte & 15));
+                    };
+                    const uint32_t ah = at(2 * h * G + g), al = at((2 * h + 1) * G + g);
+                    if constexpr (E == 8) {
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(ah), "r"(hi[0]),
+                                     "r"(hi[E / 4 - 1])
+                                     : "memory");
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(al), "r"(lo[0]),
+                                     "r"(lo[E / 4 - 1])
+                                     : "memory");
+                    } else {
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(ah), "r"(hi[0]) : "memory");
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(al), "r"(lo[0]) : "memory");
+                    }
+                    // a row with a non-finite element gives NaN logits
+                    if (lane == 0)
+                        sf[qb * 4 * G + r] = ef < 255 ? p.scale_log2 / sigma
+                                                      : __int_as_float(0x7fc00000);
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(qfull + 8 * qb);
+                if (w.g0 + w.nt >= R1)
+                    break;
+                q8_walk_next(w, p, lane);
+            }
+        }
+        if (!ok && lane == 0) {
+            report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
+            *abort_flag = 1;
+        }
+        __syncwarp();
+    } else {
+        // ================================================ softmax, epilogue
+        // outputs and the workspace may be in use by the kernel ahead
+        ptx::grid_wait_prerequisites();
+        const int rows = hpc * G;
+        // until a piece of a segment that starts in this range says otherwise
+        if (p.mode == 0 && tid == 0)
+            p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+        for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
+            const int len = p.context_lens[b];
+            if (eff_ctx(len, p.ctx_cap) > 0)
+                continue;
+            if (len != 0 && tid == 0)
+                report(p.dev_status, PA_DEV_BAD_CONTEXT);
+            uint32_t *o = reinterpret_cast<uint32_t *>(p.out + (int64_t)b * p.num_q_heads * D);
+            for (int i = tid; i < p.num_q_heads * D / 2; i += 128)
+                o[i] = 0;
+        }
+        const int hl = warp >> sub_log2;                  // this warp's head of the group
+        const int tok = ((warp & ((1 << sub_log2) - 1)) << 5) + lane;
+        const int tok0 = tok - lane;
+        const uint32_t lane_tm = (uint32_t)(warp * 32) << 16;
+        const int nk = R1 - R0;
+        float m[G], l[G], fac[G];
+        bool fail = false, seg_bad = false;
+        int seg = 0, stop = nk;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            if (fail || __all_sync(kFull, ptx::mbar_test_wait(bar, parity)))
+                return;
+            if (__any_sync(kFull, *abort_flag != 0) ||
+                !__all_sync(kFull, ptx::mbar_wait_bounded(bar, parity, lim))) {
+                fail = true;
+                if (lane == 0) {
+                    report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                __syncwarp();
+            }
+        };
+        // Each iteration holds a barrier of the four warps, also for a warp
+        // whose wait ran out; only what the barrier says ends the loop, so that
+        // all four leave it together.
+        for (int k = 0; k < nk; ++k) {
+            const int s = k % S;
+            const uint32_t s_tm = tmem + (uint32_t)((k & 1) * 64) + lane_tm;
+            wait(sfull + 8 * (k & 1), (uint32_t)((k >> 1) & 1));
+            wait(kfull + 8 * s, (uint32_t)((k / S) & 1));  // (complete: for the metadata)
+            const int qb = seg % QB;
+            bool first = false, last = false, grow = false;
+            int n = 0;
+            float e[G], x[G];
+            if (!fail) {
+                first = meta[s].first;
+                last = meta[s].last;
+                n = meta[s].n;
+                if (first) {
+                    wait(qfull + 8 * qb, (uint32_t)((seg / QB) & 1));
+                    seg_bad = false;
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        m[g] = -INFINITY;
+                        l[g] = 0.f;
+                        fac[g] = sf[qb * 4 * G + hl * G + g];
+                    }
+                    __syncwarp();
+                    if (!fail && lane == 0)
+                        ptx::mbar_arrive(qempty + 8 * qb);   // the factors are read
+                }
+                if (meta[s].bad)
+                    seg_bad = true;
+            }
+            if (!fail) {
+                ptx::tc_fence_after();
+                uint32_t u[2 * G];
+                ptx::tmem_ld<2 * G>(s_tm + (uint32_t)(hl * 2 * G), u);
+                ptx::tmem_wait_ld();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(sfree + 8 * (k & 1));
+                ptx::tmem_hold<2 * G>(u);
+                const int box = 2 * warp + (lane >> 4);
+                const float ks = meta[s].ks[box], vs = meta[s].vs[box];
+                const float lv = fmaxf(ptx::lg2(vs), -64.f);
+                const bool seen = tok < n;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float sg = (__uint_as_float(u[g]) + __uint_as_float(u[G + g])) *
+                                     (fac[g] * ks);
+                    const float mx = ptx::warp_max(seen ? sg + lv : -INFINITY);
+                    float al = 1.f;
+                    if (m[g] == -INFINITY) {
+                        m[g] = mx;                        // nothing accumulated yet
+                    } else if (mx > m[g] + kQ8Grow) {
+                        al = ptx::ex2(m[g] - mx);
+                        l[g] *= al;
+                        m[g] = mx;
+                        grow = true;
+                    }
+                    if (lane == 0)
+                        alpha_s[((k & 1) * 4 + warp) * G + g] = al;
+                    e[g] = seen ? ptx::ex2(sg - m[g]) : 0.f;
+                    l[g] += e[g];
+                    x[g] = seen ? e[g] * (vs * kQ8Weight) : 0.f;
+                }
+            }
+            grow = ptx::barrier_or(1, 128, grow || fail);
+            if (grow && ptx::barrier_or(2, 128, fail)) {
+                fail = true;
+                stop = k;
+                break;
+            }
+            // weights of tile k - 2 have been used
+            if (k >= 2)
+                wait(pvdone + 8 * (k & 1), (uint32_t)(((k >> 1) - 1) & 1));
+            if (!fail) {
+                const uint32_t pw = base + (uint32_t)(L::p_off + ((k & 1) * 4 + warp) * L::kP +
+                                                      (lane >> 4) * 128 + (lane & 15));
+                auto put = [&](int row, uint32_t v) {
+                    st_shared_u8(pw + (uint32_t)((row >> 3) * 256 + (row & 7) * 16), v);
+                };
+#pragma unroll
+                for (int g = 0; g < G; g += 2) {
+                    const float x0 = x[g], x1 = g + 1 < G ? x[g + 1 < G ? g + 1 : g] : 0.f;
+                    const float a0 = round3(x0), a1 = round3(x1);
+                    const float b0 = x0 - a0, b1 = x1 - a1;
+                    const uint32_t pa0 = e5m2x2(a0, a1), pb = e5m2x2(b0, b1);
+                    const __half2_raw bh =
+                        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pb, __NV_E5M2);
+                    const uint32_t bf = (uint32_t)bh.x | ((uint32_t)bh.y << 16);
+                    const uint32_t pc = e5m2x2(b0 - ptx::f16lo_to_f32(bf), b1 - ptx::f16hi_to_f32(bf));
+                    put(g, pa0 & 0xffu);
+                    put(GP + g, pb & 0xffu);
+                    put(2 * GP + g, pc & 0xffu);
+                    if (g + 1 < G) {
+                        put(g + 1, pa0 >> 8);
+                        put(GP + g + 1, pb >> 8);
+                        put(2 * GP + g + 1, pc >> 8);
+                    }
+                }
+                const int nv = min(max(n - tok0, 0), 32);
+                if (nv < 32) {
+                    // V rows past the sequence hold whatever was there; their
+                    // weight is 0, but 0 * NaN is NaN
+                    wait(vfull + 8 * s, (uint32_t)((k / S) & 1));
+                    const uint32_t vst =
+                        base + (uint32_t)(s * L::kStage + kQ8Tile * D + warp * 32 * D);
+                    for (int i = lane; i < (32 - nv) * (D / 16) && !fail; i += 32) {
+                        const int r = nv + i / (D / 16), c = i % (D / 16);
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         vst + (uint32_t)((r >> 3) * GROUP + (c >> 3) * 1024 +
+                                                          (r & 7) * 128 + (c & 7) * 16)),
+                                     "r"(0)
+                                     : "memory");
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+            }
+            if (grow && !first) {
+                // every accumulator column by its head's factor, once the
+                // product of tile k - 1 is in
+                wait(pvdone + 8 * ((k + 1) & 1), (uint32_t)(((k - 1) >> 1) & 1));
+                if (!fail) {
+                    ptx::tc_fence_after();
+#pragma unroll 1
+                    for (int w = 0; w < 4; ++w) {
+                        float al[G];
+#pragma unroll
+                        for (int g = 0; g < G; ++g)
+                            al[g] = alpha_s[((k & 1) * 4 + w) * G + g];
+#pragma unroll 1
+                        for (int c = 0; c < HALVES * (NP / 16); ++c) {
+                            const uint32_t at =
+                                o_tm + lane_tm + (uint32_t)(w * HALVES * NP + c * 16);
+                            uint32_t u[16];
+                            ptx::tmem_ld16(at, u);
+                            ptx::tmem_wait_ld();
+                            ptx::tmem_hold16(u);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                u[i] = __float_as_uint(__uint_as_float(u[i]) *
+                                                       ((i & (GP - 1)) < G ? al[(i & (GP - 1)) % G]
+                                                                           : 1.f));
+                            ptx::tmem_st16(at, u);
+                        }
+                    }
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                }
+            }
+            const bool cut_bad = seg_bad;
+            const Q8Meta &md = meta[s];
+            const int mb = md.b, mhg = md.hg, mj = md.j, mns = md.ns;
+            __syncwarp();
+            if (!fail && lane == 0)
+                ptx::mbar_arrive(pready + 8 * (k & 1));
+            seg += last;
+            if (!last)
+                continue;
+            // ---- the segment's share of this range is complete
+            wait(pvdone + 8 * (k & 1), (uint32_t)((k >> 1) & 1));
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    l[g] += __shfl_xor_sync(kFull, l[g], o);
+                if (lane == 0) {
+                    stat[(warp * 2) * G + g] = m[g];
+                    stat[(warp * 2 + 1) * G + g] = l[g];
+                }
+            }
+            const bool any_fail = ptx::barrier_or(2, 128, fail);
+            if (any_fail) {
+                fail = true;
+                stop = k;
+                break;
+            }
+            ptx::tc_fence_after();
+            const int segS = R0 + k - mj, segE = segS + mns;
+            const bool complete = segS >= R0 && segE <= R1;
+            const bool piece_first = segS >= R0;
+            float *ps = p.pieces + (int64_t)(2 * blockIdx.x + (piece_first ? 1 : 0)) * p.slot_floats;
+            const int subs = 1 << sub_log2;
+            if (cut_bad && complete && tid == 0)
+                report(p.dev_status, PA_DEV_BAD_BLOCK);
+#pragma unroll 1
+            for (int h = 0; h < hpc; ++h) {
+                // the head's warps joined: f = 2^(m_w - M), over the sum when
+                // the segment is complete (the weights' 2^11 cancels there)
+                float M[G], Lt[G];
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    M[g] = -INFINITY;
+                    for (int w = 0; w < subs; ++w)
+                        M[g] = fmaxf(M[g], stat[((h * subs + w) * 2) * G + g]);
+                    Lt[g] = 0.f;
+                    for (int w = 0; w < subs; ++w) {
+                        const float mw = stat[((h * subs + w) * 2) * G + g];
+                        if (mw != -INFINITY)
+                            Lt[g] += stat[((h * subs + w) * 2 + 1) * G + g] * ptx::ex2(mw - M[g]);
+                    }
+                }
+                float v[HALVES][G];
+#pragma unroll
+                for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+                        v[hf][g] = 0.f;
+#pragma unroll 1
+                for (int w = 0; w < subs; ++w) {
+                    const int vw = h * subs + w;
+                    float f[G];
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const float mw = stat[(vw * 2) * G + g];
+                        f[g] = mw == -INFINITY ? 0.f : ptx::ex2(mw - M[g]);
+                        if (complete)
+                            f[g] = Lt[g] > 0.f ? f[g] / Lt[g] : (Lt[g] == 0.f ? 0.f : Lt[g]);
+                    }
+#pragma unroll
+                    for (int hf = 0; hf < HALVES; ++hf) {
+                        uint32_t u[NP];
+#pragma unroll
+                        for (int c = 0; c < NP / 16; ++c)
+                            ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)((vw * HALVES + hf) * NP + 16 * c),
+                                           *reinterpret_cast<uint32_t(*)[16]>(&u[16 * c]));
+                        ptx::tmem_wait_ld();
+                        ptx::tmem_hold<NP>(u);
+#pragma unroll
+                        for (int g = 0; g < G; ++g)
+                            v[hf][g] += f[g] * ((__uint_as_float(u[g]) + __uint_as_float(u[GP + g])) +
+                                                __uint_as_float(u[2 * GP + g]));
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+#pragma unroll
+                    for (int hf = 0; hf < HALVES; ++hf) {
+                        const int d = hf * 128 + warp * 32 + lane;
+                        if (complete) {
+                            const float r = cut_bad ? 0.f : v[hf][g] * (1.f / kQ8Weight);
+                            p.out[((int64_t)mb * p.num_q_heads + (int64_t)mhg * rows + h * G + g) * D +
+                                  d] = __float2bfloat16_rn(r);
+                        } else {
+                            ps[(h * G + g) * D + d] = v[hf][g];
+                        }
+                    }
+                    if (!complete && tid == 0) {
+                        ps[rows * D + 2 * (h * G + g)] = M[g];
+                        ps[rows * D + 2 * (h * G + g) + 1] = Lt[g];
+                    }
+                }
+            }
+            if (!complete && tid == 0) {
+                ps[rows * D + 2 * rows] = cut_bad ? 1.f : 0.f;
+                // the CTA in whose range the segment starts names it
+                if (piece_first)
+                    p.cuts[blockIdx.x] =
+                        make_int4(mb, mhg, cta_of(segE - 1, C, total) - (int)blockIdx.x + 1, 0);
+            }
+            ptx::tc_fence_before();
+        }
+        if (stop < nk) {
+            // a wait ran out: zeros for the segments from this tile on, and a
+            // mark in their pieces
+            Q8Walk w = q8_walk_at(R0 + stop, p, cbase, lane);
+            while (true) {
+                const int segE = w.g0 + w.nt;
+                if (w.g0 >= R0 && segE <= R1) {
+                    __nv_bfloat16 *o = p.out + ((int64_t)w.b * p.num_q_heads + (int64_t)w.hg * rows) * D;
+                    for (int i = tid; i < rows * D; i += 128)
+                        o[i] = __float2bfloat16_rn(0.f);
+                } else if (tid == 0) {
+                    float *ps = p.pieces +
+                                (int64_t)(2 * blockIdx.x + (w.g0 >= R0 ? 1 : 0)) * p.slot_floats;
+                    ps[rows * D + 2 * rows] = 2.f;
+                    if (w.g0 >= R0)
+                        p.cuts[blockIdx.x] =
+                            make_int4(w.b, w.hg, cta_of(segE - 1, C, total) - (int)blockIdx.x + 1, 0);
+                }
+                if (segE >= R1)
+                    break;
+                q8_walk_next(w, p, lane);
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 4)
+        ptx::tmem_dealloc(tmem, L::tmem_cols);
+}
+
+// Joins the pieces of every segment that range borders cut: CTA (x, head,
+// part) sums 512 elements of one KV head's accumulators over the pieces of the
+// segment that starts in range x, weighted by 2^(m_i - M) / L, in piece order.
+constexpr int kQ8MaxCtas = 256;
+
+__global__ void __launch_bounds__(128) q8_merge_kernel(const Q8DecodeParams p, int G, int D,
+                                                       int parts)
+{
+    __shared__ float w[kQ8MaxCtas * 8];
+    ptx::grid_launch_dependents();
+    ptx::grid_wait_prerequisites();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int part = blockIdx.x % parts, rest = blockIdx.x / parts;
+    const int h = rest % p.hpc, x = rest / p.hpc;
+    const int4 cut = p.cuts[x];
+    const int np = cut.z;
+    if (np == 0)
+        return;
+    const int rows = p.hpc * G;
+    auto piece = [&](int i) {
+        return p.pieces + (int64_t)(i == 0 ? 2 * x + 1 : 2 * (x + i)) * p.slot_floats;
+    };
+    for (int g = warp; g < G; g += 4) {
+        const int at = rows * D + 2 * (h * G + g);
+        float M = -INFINITY, Lt = 0.f;
+        for (int i = lane; i < np; i += 32)
+            M = fmaxf(M, piece(i)[at]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+        for (int i = lane; i < np; i += 32) {
+            const float m = piece(i)[at];
+            const float f = m == -INFINITY ? 0.f : ptx::ex2(m - M);
+            w[i * 8 + g] = f;
+            if (f != 0.f)
+                Lt += piece(i)[at + 1] * f;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            Lt += __shfl_xor_sync(kFull, Lt, o);
+        const float inv = Lt > 0.f ? 1.f / (Lt * kQ8Weight) : (Lt == 0.f ? 0.f : Lt);
+        for (int i = lane; i < np; i += 32)
+            w[i * 8 + g] *= inv;
+    }
+    float flag = 0.f;
+    for (int i = tid; i < np; i += 128)
+        flag = fmaxf(flag, piece(i)[rows * D + 2 * rows]);
+    const bool bad = __syncthreads_or(flag != 0.f);      // (also: the weights are in place)
+    if (flag == 1.f && h == 0 && part == 0)
+        report(p.dev_status, PA_DEV_BAD_BLOCK);
+    const int u = part * 128 + tid;
+    if (u >= G * D / 4)
+        return;
+    const int g = u / (D / 4), d4 = u - g * (D / 4);
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!bad) {
+#pragma unroll 8
+        for (int i = 0; i < np; ++i) {
+            const float4 v =
+                __ldcg(reinterpret_cast<const float4 *>(piece(i) + (h * G + g) * D) + d4);
+            const float f = w[i * 8 + g];
+            sum.x = fmaf(v.x, f, sum.x);
+            sum.y = fmaf(v.y, f, sum.y);
+            sum.z = fmaf(v.z, f, sum.z);
+            sum.w = fmaf(v.w, f, sum.w);
+        }
+    }
+    store4(p.out + ((int64_t)cut.x * p.num_q_heads + (int64_t)cut.y * rows + h * G + g) * D + 4 * d4,
+           sum);
+}
+
+}  // namespace pa

@@ -1,0 +1,603 @@
+// pa_q8_prefill.cuh -- chunked-prefill attention over a block-scaled E4M3
+// cache on the 5th-generation tensor cores (tcgen05.mma kind::f8f6f4).  Same
+// contract as prefill_tc_kernel, with K and V the codes times their block's
+// scales, and the same structure: one CTA per (sequence, KV head, 128 query
+// rows), row r being (token r / G, query head r % G of the group).
+//
+// The codes are the B operands as the TMA brings them; nothing is converted.
+// A query row is scaled by a power of two and split into two E4M3 parts, hi
+// and lo, in tensor memory:  S = hi K^T + lo K^T.  The softmax multiplies the
+// logits of each 16-token box by its block's K scale, and the weights by its
+// block's V scale before they are split: with m a running reference of
+// s + log2 vs,
+//     x = 2^5 vs 2^(s - m) = hi + lo,
+// hi the E4M3 part (x rounded to 4 bits; 0 below 2^-6), lo the rest as E5M2
+// (3 bits, down to 2^-16):  O += hi V + lo V.  A weight is off by 2^-7 of
+// itself at most (2^-3 below 2^-6), and by 2^-17 below E5M2's range, 2^-22 of
+// the largest weight, so many small weights beside a large one are kept; row
+// sums take the fp32 weights.  The two products at twice bf16's rate cost as
+// much tensor time as one bf16 product would.
+//
+//   warps 0-3  softmax: one query row per thread
+//   warp 4     MMA issue, in the order S_{j+1}, P_{j-1} V_{j-1}
+//   warp 5     TMA of Q and K
+//   warp 6     TMA of V, block scales
+// Tensor memory columns: S [0, 64), O [64, 64 + d), Q hi and lo (d / 4 each,
+// four values per column), two weight buffers of 32 (hi 16, lo 16).
+#pragma once
+
+#include "pa_prefill.cuh"
+#include "pa_ptx8.cuh"
+
+namespace pa {
+
+struct Q8PrefillParams {
+    __nv_bfloat16 *out;
+    const float *k_scales, *v_scales;
+    const int32_t *cu_q_lens, *block_tables, *context_lens;
+    int32_t *dev_status;
+    int64_t num_blocks;
+    int total_q, num_q_heads, num_kv_heads;
+    int max_blocks, block_size, bs_log2;
+    int ctx_cap;
+    int qblocks;             // CTAs per (sequence, KV head)
+    float scale_log2;
+};
+
+constexpr int kQpRows = 128;             // query rows per CTA
+constexpr int kQpTile = 64;              // tokens per stage
+constexpr int kQpBoxes = kQpTile / 16;
+constexpr int kQpThreads = 256;
+constexpr float kQpGrow = 3.f;           // log2 growth that makes a rescale
+constexpr float kQpWeight = 32.f;        // 2^5: a weight at the reference
+constexpr float kQpSplit = 0.015625f;    // 2^-6, E4M3's smallest normal
+
+template <int D>
+struct Q8PrefillSmem {
+    static constexpr int kGroup = 8 * D;                 // bytes between 8-token groups
+    static constexpr int kBox = 16 * D;
+    static constexpr int kStage = kQpTile * D;           // K or V of a tile
+    static constexpr int kStages = D == 256 ? 5 : 8;
+    static constexpr int q_bytes = kQpRows * D * 2;      // Q as it comes (bf16)
+    static constexpr int k_off = q_bytes;
+    static constexpr int v_off = k_off + kStages * kStage;
+    static constexpr int scale_off = v_off + kStages * kStage;   // [stage][ks 4, vs 4]
+    static constexpr int bar_off = scale_off + kStages * 2 * kQpBoxes * 4;
+    // kfull, kempty, vfull, vempty [stages], pready[2], pfree[2], sfull, sfree, qfull, qready,
+    // drain
+    static constexpr int kBars = 4 * kStages + 9;
+    static constexpr int flag_off = bar_off + 8 * kBars;
+    static constexpr int bytes = 1024 + flag_off + 16;
+    static_assert(bytes <= kSmemBudget, "shared memory per CTA");
+    static constexpr uint32_t tmem_cols = 64 + D + D / 2 + 64 <= 256 ? 256u : 512u;
+    static_assert(64 + D + D / 2 + 64 <= 512, "tensor memory columns");
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(kQpThreads, 1)
+    q8_prefill_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                      const __grid_constant__ CUtensorMap tmap_k,
+                      const __grid_constant__ CUtensorMap tmap_v, const Q8PrefillParams p)
+{
+    using L = Q8PrefillSmem<D>;
+    constexpr int TQ = kQpRows / G;
+    constexpr int S = L::kStages;
+    constexpr int NCH = D / 128;                 // 128-byte columns of a token
+    constexpr uint32_t IDESC_S = ptx::umma_idesc_f8(128, kQpTile, false, false, false, false);
+    constexpr uint32_t IDESC_HI = ptx::umma_idesc_f8(128, D, false, false, false, true);
+    constexpr uint32_t IDESC_LO = ptx::umma_idesc_f8(128, D, true, false, false, true);
+
+    extern __shared__ uint8_t smem_raw[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gen = smem_raw + (base - raw);
+    float *scales = reinterpret_cast<float *>(gen + L::scale_off);
+    const uint32_t bars = base + L::bar_off;
+    const uint32_t kfull = bars, kempty = kfull + 8 * S, vfull = kempty + 8 * S,
+                   vempty = vfull + 8 * S, pready = vempty + 8 * S, pfree = pready + 16,
+                   sfull = pfree + 16, sfree = sfull + 8, qfull = sfree + 8, qready = qfull + 8,
+                   drain = qready + 8;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + L::flag_off);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen + L::flag_off + 4);
+
+    const int qb = blockIdx.x % p.qblocks;
+    const int rest = blockIdx.x / p.qblocks;
+    const int h = rest % p.num_kv_heads;
+    const int b = rest / p.num_kv_heads;
+
+    ptx::grid_wait_prerequisites();
+    const int q0 = p.cu_q_lens[b];
+    const int n = p.cu_q_lens[b + 1] - q0;
+    const int ctx = p.context_lens[b];
+    const int tok0 = qb * TQ;
+    const bool rows_ok = n >= 0 && q0 >= 0 && (int64_t)q0 + n <= p.total_q;
+    auto zero_rows = [&](int count) {
+        for (int idx = tid; idx < count * G * D; idx += kQpThreads) {
+            const int tok = idx / (G * D), r = idx - tok * G * D;
+            p.out[((int64_t)(q0 + tok0 + tok) * p.num_q_heads + h * G) * D + r] =
+                __float2bfloat16_rn(0.f);
+        }
+    };
+    if (!rows_ok || n > ctx || ctx > p.ctx_cap) {
+        if (tid == 0 && qb == 0 && h == 0)
+            report(p.dev_status, PA_DEV_BAD_CONTEXT);
+        if (rows_ok && tok0 < n)
+            zero_rows(min(TQ, n - tok0));
+        return;
+    }
+    if (tok0 >= n)
+        return;
+    const int ntok = min(TQ, n - tok0);
+    const int pos0 = ctx - n + tok0;
+    const int ntiles = (pos0 + ntok - 1) / kQpTile + 1;
+    const int last_tok = min(ntiles * kQpTile, ctx);     // tokens the tiles hold
+    const int nblk = (last_tok - 1) / p.block_size + 1;
+    auto boxes = [&](int j) { return min(kQpBoxes, (last_tok - j * kQpTile + 15) >> 4); };
+
+    if (tid == 0) {
+        for (int i = 0; i < 4 * S; ++i)
+            ptx::mbar_init(bars + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(pready + 8 * i, 4);
+            ptx::mbar_init(pfree + 8 * i, 1);
+        }
+        ptx::mbar_init(sfull, 1);
+        ptx::mbar_init(sfree, 4);
+        ptx::mbar_init(qfull, 1);
+        ptx::mbar_init(qready, 4);
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0;
+    }
+    ptx::fence_mbar_init();
+    bool bad = false;
+    const int32_t *trow = p.block_tables + (int64_t)b * p.max_blocks;
+    for (int i = tid; i < nblk; i += kQpThreads) {
+        const int id = trow[i];
+        bad |= id < 0 || (int64_t)id >= p.num_blocks;
+    }
+    if (warp == 0) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_holder), L::tmem_cols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    bad = __syncthreads_or(bad);
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const uint32_t s_tm = tmem, o_tm = tmem + 64;
+    const uint32_t qh_tm = o_tm + D, ql_tm = qh_tm + D / 4;
+    const uint32_t p_tm = ql_tm + D / 4;          // buffer s at + 32 s: hi 16 columns, lo 16
+
+    if (bad) {
+        if (tid == 0)
+            report(p.dev_status, PA_DEV_BAD_BLOCK);
+    } else if (warp == 5 || warp == 6) {
+        // ================================================== TMA producers
+        // lane x < 4 issues box x (tokens 16 x ..) of each tile
+        const bool is_k = warp == 5;
+        const uint32_t full = is_k ? kfull : vfull, empty = is_k ? kempty : vempty;
+        const void *tmap = is_k ? static_cast<const void *>(&tmap_k)
+                                : static_cast<const void *>(&tmap_v);
+        bool ok = true;
+        if (lane == 0) {
+            ptx::prefetch_tensormap(tmap);
+            if (is_k) {
+                ptx::prefetch_tensormap(&tmap_q);
+                ptx::mbar_arrive_expect_tx(qfull, (uint32_t)L::q_bytes);
+                for (int c = 0; c < D / 64; ++c)
+                    ptx::tma_load_3d_nohint(base + (uint32_t)(c * kQpRows * 128), &tmap_q, c * 64,
+                                            h * G, q0 + tok0, qfull);
+            }
+        }
+        // block ids come 32 at a time, one batch ahead
+        auto batch_ids = [&](int bt) {
+            const int i = bt * 32 + lane;
+            return i < nblk ? __ldg(trow + i) : -1;
+        };
+        int ids_cur = batch_ids(0), ids_next = batch_ids(1), cur_batch = 0;
+        // this lane's box of tile i: its block, or -1 past the context
+        auto box_id = [&](int i) {
+            const int blk = (i * kQpTile + (lane & 3) * 16) >> p.bs_log2;
+            const int from_cur = __shfl_sync(kFull, ids_cur, blk & 31);
+            const int from_next = __shfl_sync(kFull, ids_next, blk & 31);
+            const int id = (blk >> 5) == cur_batch ? from_cur : from_next;
+            return blk < nblk ? id : -1;
+        };
+        auto load_scale = [&](const float *s, int id) {
+            return id < 0 ? 0.f : __ldcg(s + (int64_t)id * p.num_kv_heads + h);
+        };
+        int id = box_id(0);
+        float ks = 0.f, vs = 0.f;
+        if (!is_k) {
+            ks = load_scale(p.k_scales, id);
+            vs = load_scale(p.v_scales, id);
+        }
+        int issued = 0;
+        for (int i = 0; i < ntiles; ++i) {
+            if (__any_sync(kFull, *abort_flag != 0))
+                break;
+            // the next tile's block and scales, a tile ahead of their use
+            const int bt = (i * kQpTile) >> (p.bs_log2 + 5);
+            if (bt != cur_batch) {
+                cur_batch = bt;
+                ids_cur = ids_next;
+                ids_next = batch_ids(bt + 1);
+            }
+            const int id_n = i + 1 < ntiles ? box_id(i + 1) : -1;
+            float ks_n = 0.f, vs_n = 0.f;
+            if (!is_k) {
+                ks_n = load_scale(p.k_scales, id_n);
+                vs_n = load_scale(p.v_scales, id_n);
+            }
+            const int s = i % S, nbox = boxes(i);
+            if (i >= S && !__all_sync(kFull, ptx::mbar_wait_bounded(
+                                                 empty + 8u * s, (uint32_t)((i / S - 1) & 1),
+                                                 kWaitLimitNs))) {
+                ok = false;
+                break;
+            }
+            const uint32_t dst = base + (uint32_t)((is_k ? L::k_off : L::v_off) + s * L::kStage);
+            if (lane == 0)
+                ptx::mbar_expect_tx(full + 8u * s, (uint32_t)(nbox * L::kBox));
+            __syncwarp();
+            if (lane < nbox) {
+                const int row = id * p.block_size + ((i * kQpTile + lane * 16) & (p.block_size - 1));
+                ptx::tma_load_5d(dst + (uint32_t)(lane * L::kBox), tmap, 0, 0, 0, row >> 3, h,
+                                 full + 8u * s, ptx::policy_evict_normal());
+            }
+            if (!is_k && lane < kQpBoxes) {
+                scales[s * 2 * kQpBoxes + lane] = ks;
+                scales[s * 2 * kQpBoxes + kQpBoxes + lane] = vs;
+            }
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(full + 8u * s);     // (also releases the scales)
+            issued = i + 1;
+            id = id_n;
+            ks = ks_n;
+            vs = vs_n;
+        }
+        if (lane == 0) {
+            if (!ok) {
+                report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // no copy may land after the CTA is gone
+            if (is_k)
+                ptx::mbar_wait_bounded(qfull, 0, kWaitLimitNs);
+            for (int i = max(0, issued - S); i < issued; ++i)
+                ptx::mbar_wait_bounded(full + 8u * (i % S), (uint32_t)((i / S) & 1), kWaitLimitNs);
+        }
+        __syncwarp();
+    } else if (warp == 4) {
+        // ====================================================== MMA issue
+        auto ready = [&](uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2) -> bool {
+            if (__all_sync(kFull, ptx::mbar_test_wait(b1, p1) && ptx::mbar_test_wait(b2, p2)))
+                return true;
+            if (__any_sync(kFull, *abort_flag != 0))
+                return false;
+            return __all_sync(kFull, ptx::mbar_wait_bounded(b1, p1, kWaitLimitNs)) &&
+                   __all_sync(kFull, ptx::mbar_wait_bounded(b2, p2, kWaitLimitNs));
+        };
+        auto issue_s = [&](int j) {
+            ptx::tc_fence_after();
+            const uint64_t kd = ptx::umma_desc_sw128(
+                base + (uint32_t)(L::k_off + (j % S) * L::kStage), 16, L::kGroup);
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk) {
+                    const uint64_t at =
+                        kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
+                    ptx::umma_f8_ts(s_tm, qh_tm + (uint32_t)(kk * 8), at, IDESC_S, kk > 0);
+                    ptx::umma_f8_ts(s_tm, ql_tm + (uint32_t)(kk * 8), at, IDESC_S, true);
+                }
+                ptx::umma_commit(sfull);
+                ptx::umma_commit(kempty + 8u * (j % S));
+            }
+            __syncwarp();
+        };
+        auto issue_pv = [&](int j) -> bool {
+            const int s = j & 1, vsn = j % S;
+            if (!ready(pready + 8u * s, (uint32_t)((j >> 1) & 1), vfull + 8u * vsn,
+                       (uint32_t)((j / S) & 1)))
+                return false;
+            ptx::tc_fence_after();
+            const int steps = (boxes(j) + 1) >> 1;       // 32 tokens each
+            const uint64_t vd = ptx::umma_desc_sw128(
+                base + (uint32_t)(L::v_off + vsn * L::kStage), 1024, L::kGroup);
+            if (ptx::elect_one()) {
+                for (int t = 0; t < steps; ++t) {
+                    const uint64_t at = vd + (uint64_t)((t * 2 * L::kBox) >> 4);
+                    const uint32_t pa0 = p_tm + (uint32_t)(s * 32 + t * 8);
+                    ptx::umma_f8_ts(o_tm, pa0, at, IDESC_HI, j > 0 || t > 0);
+                    ptx::umma_f8_ts(o_tm, pa0 + 16, at, IDESC_LO, true);
+                }
+                ptx::umma_commit(vempty + 8u * vsn);
+                ptx::umma_commit(pfree + 8u * s);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = ready(qready, 0, kfull, 0);
+        if (ok)
+            issue_s(0);
+        for (int j = 0; ok && j < ntiles; ++j) {
+            if (j + 1 < ntiles) {
+                if (!(ok = ready(sfree, (uint32_t)(j & 1), kfull + 8u * ((j + 1) % S),
+                                 (uint32_t)(((j + 1) / S) & 1))))
+                    break;
+                issue_s(j + 1);
+            }
+            if (j >= 1 && !(ok = issue_pv(j - 1)))
+                break;
+        }
+        if (ok)
+            ok = issue_pv(ntiles - 1);
+        if (!ok) {
+            if (lane == 0) {
+                report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // products already issued finish before the memory goes
+            if (ptx::elect_one())
+                ptx::umma_commit(drain);
+            __syncwarp();
+            ptx::mbar_wait_bounded(drain, 0, kWaitLimitNs);
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // =================================================== softmax warps
+        const int r = tid;                               // query row = TMEM lane
+        const int pos = min(pos0 + r / G, ctx - 1);
+        const uint32_t lane_tm = (uint32_t)(warp * 32) << 16;
+        float m_ref = -INFINITY, l = 0.f, fac = 0.f;
+        bool ok = __all_sync(kFull, ptx::mbar_wait_bounded(qfull, 0, kWaitLimitNs));
+        if (ok) {
+            // this row of Q from its swizzled copy (64-element columns of
+            // 16384 bytes): the largest element first, then both parts
+            auto unit = [&](int u8, uint32_t (&w)[4]) {     // elements 8 u8 .. 8 u8 + 7
+                const uint32_t a = base + (uint32_t)((u8 >> 3) * kQpRows * 128 + r * 128) +
+                                   ((uint32_t)((u8 & 7) ^ (r & 7)) << 4);
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(a));
+            };
+            uint32_t top = 0;
+#pragma unroll 8
+            for (int u8 = 0; u8 < D / 8; ++u8) {
+                uint32_t w[4];
+                unit(u8, w);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    top = max(top, max(w[k] << 16 & 0x7fffffffu, w[k] & 0x7fff0000u));
+            }
+            const int ef = (int)(top >> 23);
+            // (the sign of the softmax scale goes into Q, so that logit
+            // factors are not negative)
+            const float sig = __uint_as_float((uint32_t)min(254, 261 - ef) << 23);
+            const float sigma = p.scale_log2 < 0.f ? -sig : sig;
+            fac = ef < 255 ? p.scale_log2 / sigma : __int_as_float(0x7fc00000);
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                    uint32_t w[4];
+                    unit(c * 8 + v, w);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t h2[2], l2[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float y0 = ptx::bf16lo_to_f32(w[2 * k + e]) * sigma;
+                            const float y1 = ptx::bf16hi_to_f32(w[2 * k + e]) * sigma;
+                            h2[e] = f32x2_to_e4m3x2(y0, y1);
+                            const uint32_t f = e4m3x2_to_f16x2(h2[e]);
+                            l2[e] = f32x2_to_e4m3x2(y0 - ptx::f16lo_to_f32(f),
+                                                    y1 - ptx::f16hi_to_f32(f));
+                        }
+                        hi[2 * v + k] = h2[0] | (h2[1] << 16);
+                        lo[2 * v + k] = l2[0] | (l2[1] << 16);
+                    }
+                }
+                ptx::tmem_st16(qh_tm + lane_tm + (uint32_t)(c * 16), hi);
+                ptx::tmem_st16(ql_tm + lane_tm + (uint32_t)(c * 16), lo);
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(qready);
+        }
+        auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+            if (__all_sync(kFull, ptx::mbar_test_wait(bar, parity)))
+                return true;
+            if (__any_sync(kFull, *abort_flag != 0))
+                return false;
+            return __all_sync(kFull, ptx::mbar_wait_bounded(bar, parity, kWaitLimitNs));
+        };
+        for (int j = 0; ok && j < ntiles; ++j) {
+            const int s = j & 1, vsn = j % S;
+            if (!(ok = wait(sfull, (uint32_t)(j & 1))))
+                break;
+            ptx::tc_fence_after();
+            float sv[kQpTile];
+            {
+                uint32_t u0[16], u1[16], u2[16], u3[16];
+                const uint32_t sa = s_tm + lane_tm;
+                ptx::tmem_ld16(sa, u0);
+                ptx::tmem_ld16(sa + 16, u1);
+                ptx::tmem_ld16(sa + 32, u2);
+                ptx::tmem_ld16(sa + 48, u3);
+                ptx::tmem_wait_ld();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(sfree);
+                ptx::tmem_hold16(u0);
+                ptx::tmem_hold16(u1);
+                ptx::tmem_hold16(u2);
+                ptx::tmem_hold16(u3);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    sv[e] = __uint_as_float(u0[e]);
+                    sv[16 + e] = __uint_as_float(u1[e]);
+                    sv[32 + e] = __uint_as_float(u2[e]);
+                    sv[48 + e] = __uint_as_float(u3[e]);
+                }
+            }
+            // V_j is in: so are the tile's block scales
+            if (!(ok = wait(vfull + 8u * vsn, (uint32_t)((j / S) & 1))))
+                break;
+            float kf[kQpBoxes], vw[kQpBoxes], lv[kQpBoxes];
+#pragma unroll
+            for (int x = 0; x < kQpBoxes; ++x) {
+                const float f = fac * scales[vsn * 2 * kQpBoxes + x];
+                const float v = scales[vsn * 2 * kQpBoxes + kQpBoxes + x];
+                kf[x] = f == 0.f ? 1.2e-38f : f;         // (a masked -inf stays one)
+                vw[x] = v * kQpWeight;
+                lv[x] = fmaxf(ptx::lg2(v), -64.f);
+            }
+            const int tstart = j * kQpTile;
+            if (tstart + kQpTile - 1 > pos0) {
+#pragma unroll
+                for (int c = 0; c < kQpTile; ++c)
+                    sv[c] = tstart + c <= pos ? sv[c] : -INFINITY;
+            }
+            float mx = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < kQpBoxes; ++x) {
+                float a = sv[16 * x], c = sv[16 * x + 1];
+#pragma unroll
+                for (int e = 2; e < 16; e += 2) {
+                    a = fmaxf(a, sv[16 * x + e]);
+                    c = fmaxf(c, sv[16 * x + e + 1]);
+                }
+                mx = fmaxf(mx, fmaf(fmaxf(a, c), kf[x], lv[x]));
+            }
+            bool grow = false;
+            float alpha = 1.f;
+            if (m_ref == -INFINITY) {
+                m_ref = mx;
+            } else if (mx > m_ref + kQpGrow) {
+                grow = true;
+                alpha = ptx::ex2(m_ref - mx);
+            }
+            if (__any_sync(kFull, grow)) {
+                // P_{j-1} V_{j-1} (and all before) must be in O
+                if (!(ok = wait(pfree + 8u * (s ^ 1), (uint32_t)(((j - 1) >> 1) & 1))))
+                    break;
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t u[16];
+                    ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 16), u);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_hold16(u);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+                    ptx::tmem_st16(o_tm + lane_tm + (uint32_t)(c * 16), u);
+                }
+                ptx::tmem_wait_st();
+            }
+            if (grow) {
+                l *= alpha;
+                m_ref = mx;
+            }
+            const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
+            uint32_t hi[16], lo[16];
+            float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const int x = k >> 2;
+                float e[4], a[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    e[i] = ptx::ex2(fmaf(sv[4 * k + i], kf[x], nref));
+                    l4[i] += e[i];
+                    e[i] *= vw[x];
+                    // 4 bits, to nearest; nothing below E4M3's normals
+                    a[i] = e[i] < kQpSplit
+                               ? 0.f
+                               : __uint_as_float((__float_as_uint(e[i]) + 0x80000u) & 0xfff00000u);
+                }
+                hi[k] = f32x2_to_e4m3x2(a[0], a[1]) | (f32x2_to_e4m3x2(a[2], a[3]) << 16);
+                lo[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(e[0] - a[0], e[1] - a[1]),
+                                                           __NV_SATFINITE, __NV_E5M2) |
+                        ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(e[2] - a[2], e[3] - a[3]),
+                                                            __NV_SATFINITE, __NV_E5M2)
+                         << 16);
+            }
+            l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+            if (j >= 2) {
+                if (!(ok = wait(pfree + 8u * s, (uint32_t)(((j - 2) >> 1) & 1))))
+                    break;
+                ptx::tc_fence_after();
+            }
+            ptx::tmem_st16(p_tm + lane_tm + (uint32_t)(s * 32), hi);
+            ptx::tmem_st16(p_tm + lane_tm + (uint32_t)(s * 32 + 16), lo);
+            if (tstart + kQpTile > last_tok && ((last_tok - tstart) & 31) != 0) {
+                // V rows of the last 32-token step past the context: their
+                // weight is 0, but 0 * NaN is NaN
+                const int from = last_tok - tstart, to = (from + 31) & ~31;
+                const uint32_t vst = base + (uint32_t)(L::v_off + vsn * L::kStage);
+                for (int idx = r; idx < (to - from) * NCH * 8; idx += kQpRows) {
+                    const int t = from + idx / (NCH * 8), c = idx % (NCH * 8);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                     vst + (uint32_t)((t >> 3) * L::kGroup + (c >> 3) * 1024 +
+                                                      (t & 7) * 128 + (c & 7) * 16)),
+                                 "r"(0)
+                                 : "memory");
+                }
+                ptx::fence_proxy_async_smem();
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(pready + 8u * s);
+        }
+        if (ok && !wait(pfree + 8u * ((ntiles - 1) & 1), (uint32_t)(((ntiles - 1) >> 1) & 1)))
+            ok = false;
+        if (!ok) {
+            if (lane == 0) {
+                report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
+                *abort_flag = 1;
+            }
+            __syncwarp();
+        } else {
+            ptx::tc_fence_after();
+            // (a sum that is not a number, from a non-finite query, stays one)
+            const float inv = l == 0.f ? 0.f : __frcp_rn(l) * (1.f / kQpWeight);
+            const bool store = r / G < ntok;
+            uint4 *dst = reinterpret_cast<uint4 *>(
+                p.out + ((int64_t)(q0 + tok0 + (store ? r / G : 0)) * p.num_q_heads + h * G + r % G) * D);
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t u[16], o[8];
+                ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 16), u);
+                ptx::tmem_wait_ld();
+                ptx::tmem_hold16(u);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    o[k] = ptx::pack_bf16x2(__uint_as_float(u[2 * k]) * inv,
+                                            __uint_as_float(u[2 * k + 1]) * inv);
+                if (store) {
+                    dst[2 * c] = make_uint4(o[0], o[1], o[2], o[3]);
+                    dst[2 * c + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    // zeros for an invalid block and for a wait that ran out
+    if (bad || *abort_flag != 0)
+        zero_rows(ntok);
+    if (warp == 0)
+        ptx::tmem_dealloc(tmem, L::tmem_cols);
+}
+
+}  // namespace pa

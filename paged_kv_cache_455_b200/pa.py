@@ -32,6 +32,7 @@ _F = ctypes.c_float
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_WORKSPACE = range(5)
 PA_DTYPE_F32, PA_DTYPE_BF16, PA_DTYPE_FP8_E4M3 = 0, 1, 2
 PA_DEV_BAD_SLOT, PA_DEV_BAD_BLOCK, PA_DEV_BAD_CONTEXT, PA_DEV_WAIT_TIMEOUT = 1, 2, 4, 8
+PA_DEV_BAD_POSITION = 16
 
 # Every symbol include/pa.h declares, with its C signature.
 SIGNATURES = {
@@ -53,6 +54,17 @@ SIGNATURES = {
     "pa_reshape_and_cache_fp8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I64, _F, _F, _P, _P]),
     "pa_decode_attention_fp8": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I64, _F,
                                      _F, _F, _P, _SZ, _P, _P]),
+    "pa_rope_and_cache": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I,
+                               _I64, _I, _I, _I, _I, _I, _I, _I64, _I, _P, _P]),
+    "pa_rope_and_cache_q8": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I,
+                                  _I, _P, _I, _P, _I, _P, _P, _I, _I64, _I, _I, _I, _I, _I, _I64,
+                                  _P, _P]),
+    "pa_decode_attention_q8": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I,
+                                    _I64, _F, _P, _SZ, _P, _P]),
+    "pa_prefill_attention_q8": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I,
+                                     _I, _I, _I, _I64, _F, _P, _P]),
+    "pa_copy_blocks_q8": (_I, [_P, _P, _P, _P, _I64, _P, _P, _P, _P, _I64, _P, _I, _I, _I, _I,
+                               _P, _P]),
     "pa_status_string": (ctypes.c_char_p, [_I]),
     "pa_launch_count": (ctypes.c_ulonglong, []),
     # include/pa_testing.h
@@ -361,6 +373,212 @@ def pa_splitk_reduce(out: torch.Tensor, tmp_out: torch.Tensor, max_logits: torch
                                 _dtype_code(out), _stream(stream)), "pa_splitk_reduce")
 
 
+def rope_table(max_position: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The cos_sin table [max_position, rot_dim] fp32 of the usual frequencies,
+    base^(-2 i / rot_dim): cosines, then sines; the angles are taken in fp64."""
+    inv = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    ang = torch.arange(max_position, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([ang.cos(), ang.sin()], dim=1).float().contiguous()
+
+
+def _token_rows(t: torch.Tensor, name: str, total: int, d: int, dtype) -> int:
+    """Elements between tokens of t [total, heads, d], whose heads are dense."""
+    if not t.is_cuda or t.dim() != 3 or t.shape[0] != total or t.shape[2] != d or t.dtype != dtype:
+        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, {d}] of {dtype}")
+    heads = t.shape[1]
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"the heads of {name} must be dense")
+    return t.stride(0) if total > 1 else max(heads, 1) * d
+
+
+def _rope_args(query_out, query, key, value, positions, cos_sin, dtype):
+    """Checks what both rotary cache writes share; returns the pointer and
+    stride arguments, the rotation arguments and (T, hq, hkv, d)."""
+    if key.dim() != 3:
+        raise ValueError("key must be [tokens, Hkv, d]")
+    T, hkv, d = key.shape
+    ks = _token_rows(key, "key", T, d, dtype)
+    vs = _token_rows(value, "value", T, d, dtype)
+    if value.shape != key.shape:
+        raise ValueError("shape mismatch")
+    hq = qs = qos = 0
+    if (query is None) != (query_out is None):
+        raise ValueError("query and query_out go together")
+    if query is not None:
+        qs = _token_rows(query, "query", T, d, dtype)
+        qos = _token_rows(query_out, "query_out", T, d, dtype)
+        if query_out.shape != query.shape:
+            raise ValueError("shape mismatch")
+        hq = query.shape[1]
+    rot = max_pos = 0
+    if cos_sin is not None:
+        _cuda(cos_sin, positions)
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be float32 [max_position, rot_dim]")
+        if positions is None or positions.dtype != torch.int64 or positions.shape != (T,):
+            raise ValueError("positions must be int64 [tokens]")
+        max_pos, rot = cos_sin.shape
+    elif positions is not None:
+        raise ValueError("positions need cos_sin")
+    rows = (_ptr(query_out), qos, _ptr(query), qs, _ptr(key), ks, _ptr(value), vs)
+    return rows, (_ptr(positions), _ptr(cos_sin), rot, max_pos), (T, hq, hkv, d)
+
+
+def pa_rope_and_cache(query_out: Optional[torch.Tensor], query: Optional[torch.Tensor],
+                      key: torch.Tensor, value: torch.Tensor, k_pool: torch.Tensor,
+                      v_pool: torch.Tensor, slot_mapping: torch.Tensor,
+                      positions: Optional[torch.Tensor] = None,
+                      cos_sin: Optional[torch.Tensor] = None, interleaved: bool = False,
+                      dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """query/query_out [T, Hq, d] (or both None; query_out may be query),
+    key/value [T, Hkv, d], tokens at any stride; pools [nb, bs, Hkv, d];
+    slot_mapping, positions [T] int64; cos_sin [max_position, rot_dim] fp32
+    (None: nothing is rotated)."""
+    _cuda(k_pool, v_pool, slot_mapping, dev_status)
+    rows, rot, (T, hq, hkv, d) = _rope_args(query_out, query, key, value, positions, cos_sin,
+                                            k_pool.dtype)
+    nb, bs = k_pool.shape[:2]
+    if v_pool.shape != k_pool.shape or v_pool.dtype != k_pool.dtype or \
+            k_pool.shape[2:] != (hkv, d):
+        raise ValueError("pool mismatch")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be int64 [T]")
+    _check(lib.pa_rope_and_cache(*rows, _ptr(k_pool), _ptr(v_pool), _ptr(slot_mapping), *rot,
+                                 int(bool(interleaved)), T, hq, hkv, d, bs, nb,
+                                 _dtype_code(k_pool), _ptr(dev_status), _stream(stream)),
+           "pa_rope_and_cache")
+
+
+def _q8_pools(k_pool, v_pool, k_scales, v_scales):
+    """Checks one side's block-scaled pools; returns (nb, bs, hkv, d)."""
+    if k_pool.dim() != 4 or v_pool.shape != k_pool.shape:
+        raise ValueError("pools must be [nb, bs, Hkv, d]")
+    if k_pool.dtype not in FP8_POOL_DTYPES or v_pool.dtype not in FP8_POOL_DTYPES:
+        raise ValueError("pools must hold E4M3 codes (uint8 or float8_e4m3fn)")
+    nb, bs, hkv, d = k_pool.shape
+    for s in (k_scales, v_scales):
+        if s.dtype != torch.float32 or s.shape != (nb, hkv):
+            raise ValueError("scales must be float32 [nb, Hkv]")
+    return nb, bs, hkv, d
+
+
+def _tables(block_tables, context_lens, B):
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be int32 [B, max_blocks]")
+    if context_lens.dtype != torch.int32 or context_lens.shape != (B,):
+        raise ValueError("context_lens must be int32 [B]")
+
+
+def pa_rope_and_cache_q8(query_out: Optional[torch.Tensor], query: Optional[torch.Tensor],
+                         key: torch.Tensor, value: torch.Tensor, k_pool: torch.Tensor,
+                         v_pool: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                         cu_q_lens: torch.Tensor, max_q_len: int, block_tables: torch.Tensor,
+                         context_lens: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                         cos_sin: Optional[torch.Tensor] = None, interleaved: bool = False,
+                         dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """As pa_rope_and_cache, bf16, into pools of E4M3 codes (uint8 or
+    float8_e4m3fn) with scales [nb, Hkv] fp32: sequence b appends rows
+    cu_q_lens[b] .. cu_q_lens[b + 1] - 1, the last of its context_lens[b]
+    cached tokens.  cu_q_lens [B + 1], block_tables [B, max_blocks],
+    context_lens [B] int32."""
+    _cuda(k_pool, v_pool, k_scales, v_scales, cu_q_lens, block_tables, context_lens, dev_status)
+    rows, rot, (T, hq, hkv, d) = _rope_args(query_out, query, key, value, positions, cos_sin,
+                                            torch.bfloat16)
+    nb, bs, phkv, pd = _q8_pools(k_pool, v_pool, k_scales, v_scales)
+    if (phkv, pd) != (hkv, d):
+        raise ValueError("pool mismatch")
+    B = context_lens.shape[0]
+    _tables(block_tables, context_lens, B)
+    if cu_q_lens.dtype != torch.int32 or cu_q_lens.shape != (B + 1,):
+        raise ValueError("cu_q_lens must be int32 [B + 1]")
+    _check(lib.pa_rope_and_cache_q8(*rows, _ptr(k_pool), _ptr(v_pool), _ptr(k_scales),
+                                    _ptr(v_scales), _ptr(cu_q_lens), T, int(max_q_len),
+                                    _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+                                    B, *rot, int(bool(interleaved)), hq, hkv, d, bs, nb,
+                                    _ptr(dev_status), _stream(stream)), "pa_rope_and_cache_q8")
+
+
+def pa_decode_attention_q8(out: torch.Tensor, query: torch.Tensor, k_pool: torch.Tensor,
+                           v_pool: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                           block_tables: torch.Tensor, context_lens: torch.Tensor,
+                           max_context_len: int, scale: float,
+                           workspace: Optional[torch.Tensor] = None,
+                           dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out, query [B, Hq, d] bf16; pools [nb, bs, Hkv, d] of E4M3 codes with
+    scales [nb, Hkv] fp32; block_tables [B, max_blocks], context_lens [B]
+    int32; workspace as in pa_decode_attention."""
+    _cuda(out, query, k_pool, v_pool, k_scales, v_scales, block_tables, context_lens, workspace,
+          dev_status)
+    B, hq, d = query.shape
+    nb, bs, hkv, pd = _q8_pools(k_pool, v_pool, k_scales, v_scales)
+    if out.shape != query.shape or pd != d:
+        raise ValueError("shape mismatch")
+    if query.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+        raise ValueError("query and out must be bf16")
+    _tables(block_tables, context_lens, B)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.pa_decode_attention_q8(_ptr(out), _ptr(query), _ptr(k_pool), _ptr(v_pool),
+                                      _ptr(k_scales), _ptr(v_scales), _ptr(block_tables),
+                                      block_tables.shape[1], _ptr(context_lens), B,
+                                      int(max_context_len), hq, hkv, d, bs, nb, float(scale),
+                                      _ptr(workspace), ws_bytes, _ptr(dev_status),
+                                      _stream(stream)), "pa_decode_attention_q8")
+
+
+def pa_prefill_attention_q8(out: torch.Tensor, query: torch.Tensor, cu_q_lens: torch.Tensor,
+                            max_q_len: int, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                            k_scales: torch.Tensor, v_scales: torch.Tensor,
+                            block_tables: torch.Tensor, context_lens: torch.Tensor,
+                            max_context_len: int, scale: float,
+                            dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """query/out [total_q, Hq, d] bf16; cu_q_lens [B + 1] int32; pools, scales,
+    tables and lengths as in pa_decode_attention_q8."""
+    _cuda(out, query, cu_q_lens, k_pool, v_pool, k_scales, v_scales, block_tables, context_lens,
+          dev_status)
+    total_q, hq, d = query.shape
+    nb, bs, hkv, pd = _q8_pools(k_pool, v_pool, k_scales, v_scales)
+    B = context_lens.shape[0]
+    if out.shape != query.shape or pd != d:
+        raise ValueError("shape mismatch")
+    if query.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+        raise ValueError("query and out must be bf16")
+    _tables(block_tables, context_lens, B)
+    if cu_q_lens.dtype != torch.int32 or cu_q_lens.shape != (B + 1,):
+        raise ValueError("cu_q_lens must be int32 [B + 1]")
+    _check(lib.pa_prefill_attention_q8(_ptr(out), _ptr(query), _ptr(cu_q_lens), total_q,
+                                       int(max_q_len), _ptr(k_pool), _ptr(v_pool),
+                                       _ptr(k_scales), _ptr(v_scales), _ptr(block_tables),
+                                       block_tables.shape[1], _ptr(context_lens), B,
+                                       int(max_context_len), hq, hkv, d, bs, nb, float(scale),
+                                       _ptr(dev_status), _stream(stream)),
+           "pa_prefill_attention_q8")
+
+
+def pa_copy_blocks_q8(dst_k: torch.Tensor, dst_v: torch.Tensor, dst_k_scales: torch.Tensor,
+                      dst_v_scales: torch.Tensor, src_k: torch.Tensor, src_v: torch.Tensor,
+                      src_k_scales: torch.Tensor, src_v_scales: torch.Tensor,
+                      block_mapping: torch.Tensor, dev_status: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """Copies block src -> dst with its scales for each (src, dst) row of
+    block_mapping [P, 2] int64, from the source's block-scaled pools to the
+    destination's (the same ones, or either side in pinned host memory)."""
+    for t in (dst_k, dst_v, dst_k_scales, dst_v_scales, src_k, src_v, src_k_scales, src_v_scales):
+        if not t.is_contiguous() or not (t.is_cuda or t.is_pinned()):
+            raise ValueError("pools and scales must be contiguous CUDA or pinned host tensors")
+    _cuda(block_mapping, dev_status)
+    dnb, bs, hkv, d = _q8_pools(dst_k, dst_v, dst_k_scales, dst_v_scales)
+    snb, *same = _q8_pools(src_k, src_v, src_k_scales, src_v_scales)
+    if same != [bs, hkv, d]:
+        raise ValueError("pool shape mismatch")
+    if block_mapping.dtype != torch.int64 or block_mapping.dim() != 2 or block_mapping.shape[1] != 2:
+        raise ValueError("block_mapping must be int64 [P, 2]")
+    _check(lib.pa_copy_blocks_q8(_ptr(dst_k), _ptr(dst_v), _ptr(dst_k_scales), _ptr(dst_v_scales),
+                                 dnb, _ptr(src_k), _ptr(src_v), _ptr(src_k_scales),
+                                 _ptr(src_v_scales), snb, _ptr(block_mapping),
+                                 block_mapping.shape[0], bs, hkv, d, _ptr(dev_status),
+                                 _stream(stream)), "pa_copy_blocks_q8")
+
+
 __all__ = [
     "lib", "LIB_PATH", "SIGNATURES", "PaError", "launch_count",
     "pa_reshape_and_cache", "pa_reshape_and_cache_fp8", "pa_decode_attention_fp8",
@@ -369,5 +587,7 @@ __all__ = [
     "pa_num_partitions", "pa_splitk_workspace_bytes", "pa_decode_splitk", "pa_splitk_reduce",
     "PA_OK", "PA_ERR_INVALID_ARG", "PA_ERR_UNSUPPORTED", "PA_ERR_CUDA", "PA_ERR_WORKSPACE",
     "PA_DTYPE_F32", "PA_DTYPE_BF16", "PA_DTYPE_FP8_E4M3",
+    "rope_table", "pa_rope_and_cache", "pa_rope_and_cache_q8", "pa_decode_attention_q8",
+    "pa_prefill_attention_q8", "pa_copy_blocks_q8", "PA_DEV_BAD_POSITION",
     "PA_DEV_BAD_SLOT", "PA_DEV_BAD_BLOCK", "PA_DEV_BAD_CONTEXT", "PA_DEV_WAIT_TIMEOUT",
 ]
