@@ -23,7 +23,7 @@ pa_status run(Launch &L, bool launch)
     auto fn = &pa::q8_decode_kernel<D, G>;
     constexpr int smem = pa::Q8Smem<D, G>::bytes;
     int cap = 0;
-    const pa_status st = pa::grid_capacity(reinterpret_cast<const void *>(fn), pa::kQ8Threads,
+    const pa_status st = pa::grid_capacity(reinterpret_cast<const void *>(fn), pa::Q8Smem<D, G>::kThreads,
                                            smem, &cap);
     if (st != PA_OK)
         return st;
@@ -31,7 +31,7 @@ pa_status run(Launch &L, bool launch)
         L.grid = std::min(cap, pa::kQ8MaxCtas);
         return PA_OK;
     }
-    return pa::launch_dependent(fn, (unsigned)L.grid, pa::kQ8Threads, smem, L.stream, L.tk, L.tv,
+    return pa::launch_dependent(fn, (unsigned)L.grid, pa::Q8Smem<D, G>::kThreads, smem, L.stream, L.tk, L.tv,
                                 L.p);
 }
 
@@ -99,6 +99,7 @@ extern "C" pa_status pa_decode_attention_q8(void *out, const void *query, const 
     p.hpc_log2 = num_kv_heads % 4 == 0 ? 2 : (num_kv_heads % 2 == 0 ? 1 : 0);
     p.hpc = 1 << p.hpc_log2;
     p.tt_log2 = 7 - p.hpc_log2;
+    p.box_log2 = block_size == 32 ? 5 : 4;
     p.head_groups = num_kv_heads / p.hpc;
     p.scale_log2 = scale * pa::kLog2e;
     const unsigned long long wait_ns = pa::test_wait_ns();
@@ -106,9 +107,9 @@ extern "C" pa_status pa_decode_attention_q8(void *out, const void *query, const 
     p.withhold_cta = pa::test_withhold_cta();
     L.stream = stream;
     if (!pa::pool_map_grouped(&L.tk, k_pool, num_blocks, block_size, num_kv_heads, head_dim,
-                              PA_DTYPE_FP8_E4M3, 16) ||
+                              PA_DTYPE_FP8_E4M3, block_size) ||
         !pa::pool_map_grouped(&L.tv, v_pool, num_blocks, block_size, num_kv_heads, head_dim,
-                              PA_DTYPE_FP8_E4M3, 16))
+                              PA_DTYPE_FP8_E4M3, block_size))
         return PA_ERR_CUDA;
     st = run_any(L, head_dim, group, false);
     if (st != PA_OK)

@@ -19,21 +19,30 @@
 // so no code is ever converted or moved by a thread, and the softmax of one
 // tile is 32 tokens per warp, one per lane.
 //
-// Weights.  x_t = 2^11 vs(t) 2^(s_t - m) with m a running reference per head
-// and warp, at least max_t (s_t + log2 vs(t)) - 4 (log2 units): x_t <= 2^15.
-// The three E5M2 parts are the value rounded to 3 bits, the rest rounded to
-// 3, and again: error 2^-9 of x_t down to x_t = 2^-8 and 2^-17 below, that is
-// 2^-28 of the largest weight, so that many small weights next to a large one
-// are not lost.  The row sums take the fp32 weights 2^(s_t - m).  Because m
-// follows the weights with their scales, the errors are relative to what the
-// output is made of, whatever the scales' spread.
+// Weights.  x_t = 2^7 vs(t) 2^(s_t - m) with m a running reference per head
+// and warp, raised to max_t (s_t + log2 vs(t)) whenever that has grown past
+// m + 8 (log2 units): x_t <= 2^15.  The three E5M2 parts are the value rounded
+// to 3 bits, the rest rounded to 3, and again: error 2^-9 of x_t down to
+// x_t = 2^-8 and 2^-17 below, that is 2^-24 of the largest weight, so that many
+// small weights next to a large one are not lost.  The row sums take the fp32
+// weights 2^(s_t - m).  Because m follows the weights with their scales, the
+// errors are relative to what the output is made of, whatever the scales'
+// spread.  A warp needs the maximum itself only for its first tile and when a
+// vote finds a lane past the reference, and accumulators are rescaled only then.
 //
-// Warps: 0-3 softmax and epilogue, 4 MMA issue, 5 TMA and block scales, 6-7
-// query rows.  Work is split as in decode_kernel: every CTA owns an equal,
-// contiguous range of the batch's tiles (mode 0), or whole segments (mode 1);
-// a segment is the run of tiles of one sequence and head group.  The pieces
-// of a segment cut by range borders go to the workspace as fp32 (maximum, sum,
-// accumulator), and q8_merge_kernel joins them after this kernel.
+// Warps: SETS x 4 softmax and epilogue, then one each for S, O^T, the TMA of K,
+// the TMA of V with the block scales, and two for the query rows.  The softmax
+// of a tile is a chain of latencies (~1100 cycles at G = 4), longer than a
+// tile's share of the memory bandwidth (1450 cycles at d = 256, 725 at
+// d = 128), so two sets of warps take alternate tiles, each with accumulators
+// and references of its own; they are joined at the segment's end.  With
+// d = 256 and G = 8 tensor memory holds one set's accumulators only.
+//
+// Work is split as in decode_kernel: every CTA owns an equal, contiguous range
+// of the batch's tiles (mode 0), or whole segments (mode 1); a segment is the
+// run of tiles of one sequence and head group.  The pieces of a segment cut by
+// range borders go to the workspace as fp32 (maximum, sum, accumulator), and
+// q8_merge_kernel joins them after this kernel.
 #pragma once
 
 #include "pa_kernels.cuh"
@@ -41,11 +50,10 @@
 
 namespace pa {
 
-constexpr int kQ8Threads = 256;
 constexpr int kQ8Tile = 128;              // rows of K and V per tile (MMA M)
 constexpr int kQ8SmemStages = 6 * 32768;  // bytes of the stage ring
-constexpr float kQ8Grow = 4.f;            // log2 growth that makes a rescale
-constexpr float kQ8Weight = 2048.f;       // 2^11: a weight at the reference
+constexpr float kQ8Grow = 8.f;            // log2 growth that makes a rescale
+constexpr float kQ8Weight = 128.f;        // 2^7: a weight at the reference
 
 struct Q8DecodeParams {
     __nv_bfloat16 *out;
@@ -61,6 +69,7 @@ struct Q8DecodeParams {
     int ctx_cap;
     int hpc, hpc_log2;       // KV heads per tile
     int tt_log2;             // tokens per tile = 128 / hpc
+    int box_log2;            // tokens per TMA box: 16, or 32 with blocks of 32
     int head_groups;
     int mode;                // 0: equal ranges, 1: whole segments
     int slot_floats;
@@ -69,39 +78,47 @@ struct Q8DecodeParams {
     int withhold_cta;        // test hook, as in DecodeParams
 };
 
-// Per-stage metadata, written by the TMA warp with the stage.
+// Per-stage metadata, written by V's TMA warp.
 struct Q8Meta {
     int b, hg, j, ns;        // sequence, head group, tile in the segment, its tiles
     int n;                   // valid tokens of the tile
-    int first, last;         // first / last tile of the segment in this CTA's range
+    int seg;                 // ordinal of the segment in this CTA's range
     int bad;                 // an invalid block id
+    int pad;
     float ks[8], vs[8];      // scales of the tile's 16-row boxes
 };
 
 template <int D, int G>
 struct Q8Smem {
-    static constexpr int kStage = 2 * kQ8Tile * D;
-    static constexpr int kStages = kQ8SmemStages / kStage;           // 3 (d 256), 6 (d 128)
+    static constexpr int kStage = kQ8Tile * D;                       // K or V of a tile
+    static constexpr int kStages = kQ8SmemStages / (2 * kStage);     // 3 (d 256), 6 (d 128)
     static constexpr int kQRows = 8 * G < 16 ? 16 : 8 * G;           // up to 4 heads, 2 parts
     static constexpr int kQBufs = (D == 256 && G == 8) ? 1 : 2;
     static constexpr int GP = G <= 4 ? 4 : 8;                        // rows of one weight part
     static constexpr int NP = 4 * GP;                                // 3 parts, padded
     static constexpr int kP = NP * 32;                               // bytes of a warp's weights
+    // tensor memory columns: two S buffers of 64, then the sets' accumulators
+    static constexpr int o_cols = 4 * (D / 128) * NP;
+    static constexpr int kSets = 128 + 2 * o_cols <= 512 ? 2 : 1;
+    static constexpr uint32_t tmem_cols = 128 + kSets * o_cols <= 256 ? 256u : 512u;
+    static constexpr int kSoftmax = 4 * kSets;                       // warps
+    static constexpr int kThreads = 32 * (kSoftmax + 6);
+    static constexpr int v_off = kStages * kStage;
     static constexpr int q_off = kQ8SmemStages;
     static constexpr int p_off = q_off + kQBufs * kQRows * D;
     static constexpr int meta_off = p_off + 2 * 4 * kP;
-    static constexpr int sf_off = meta_off + kStages * (int)sizeof(Q8Meta);
-    static constexpr int stat_off = sf_off + kQBufs * 4 * G * 4;     // m, l per warp and head
-    static constexpr int alpha_off = stat_off + 4 * 2 * G * 4;
-    static constexpr int bar_off = (alpha_off + 2 * 4 * G * 4 + 15) / 16 * 16;
-    static constexpr int kBars = 3 * kStages + 8 + 2 * kQBufs + 1;
-    static constexpr int flag_off = bar_off + 8 * kBars;
+    static constexpr int kflag_off = meta_off + kStages * (int)sizeof(Q8Meta);
+    static constexpr int sf_off = kflag_off + 4 * 8;                 // query factors of 4 segments
+    static constexpr int stat_off = sf_off + 4 * 4 * G * 4;          // [2][sets][4][m, l][G]
+    static constexpr int fac_off = stat_off + 2 * kSets * 4 * 2 * G * 4;   // [sets][4][G]
+    static constexpr int alpha_off = fac_off + kSets * 4 * G * 4;    // [sets][4][G]
+    static constexpr int cut_off = (alpha_off + kSets * 4 * G * 4 + 15) / 16 * 16;
+    static constexpr int bar_off = cut_off + 16;
+    static constexpr int kBars = 5 * kStages + 8 + 2 * kQBufs + 5;
+    static constexpr int flag_off = bar_off + 8 * kBars;   // abort, tensor memory, tiles done
     static constexpr int cbase_off = flag_off + 16;
     static constexpr int bytes = 1024 + cbase_off + 4 * (kMaxChunks + 1);
     static_assert(bytes <= kSmemBudget, "shared memory per CTA");
-    // tensor memory columns: two S buffers of 64, then the accumulators
-    static constexpr int o_cols = 4 * (D / 128) * NP;
-    static constexpr uint32_t tmem_cols = 128 + o_cols <= 256 ? 256u : 512u;
 };
 
 // Position in the batch's sequence of segments (whole warp, uniform).
@@ -232,60 +249,68 @@ __device__ __forceinline__ void st_shared_u8(uint32_t a, uint32_t v)
 }
 
 template <int D, int G>
-__global__ void __launch_bounds__(kQ8Threads, 1)
+__global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
     q8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, const Q8DecodeParams p)
 {
     using L = Q8Smem<D, G>;
-    constexpr int S = L::kStages, QB = L::kQBufs, GP = L::GP, NP = L::NP;
+    constexpr int S = L::kStages, QB = L::kQBufs, GP = L::GP, NP = L::NP, SETS = L::kSets;
     constexpr int HALVES = D / 128;
     constexpr int GROUP = 8 * D;                 // bytes between 8-row groups
+    constexpr int W_S = L::kSoftmax, W_O = W_S + 1, W_K = W_S + 2, W_V = W_S + 3, W_Q = W_S + 4;
     extern __shared__ uint8_t smem_raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *gen = smem_raw + (base - raw);
     Q8Meta *meta = reinterpret_cast<Q8Meta *>(gen + L::meta_off);
+    volatile int *kflag = reinterpret_cast<volatile int *>(gen + L::kflag_off);
     float *sf = reinterpret_cast<float *>(gen + L::sf_off);
     float *stat = reinterpret_cast<float *>(gen + L::stat_off);
+    float *fac_s = reinterpret_cast<float *>(gen + L::fac_off);
     float *alpha_s = reinterpret_cast<float *>(gen + L::alpha_off);
+    int4 *cut_s = reinterpret_cast<int4 *>(gen + L::cut_off);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + L::flag_off);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen + L::flag_off + 4);
+    volatile int *tiles_done = reinterpret_cast<volatile int *>(gen + L::flag_off + 8);
     int *cbase = reinterpret_cast<int *>(gen + L::cbase_off);
     const uint32_t bars = base + L::bar_off;
-    const uint32_t kfull = bars, vfull = kfull + 8 * S, empty = vfull + 8 * S,
-                   sfull = empty + 8 * S, sfree = sfull + 16, pready = sfree + 16,
-                   pvdone = pready + 16, qfull = pvdone + 16, qempty = qfull + 8 * QB,
-                   drain = qempty + 8 * QB;
+    const uint32_t kfull = bars, kempty = kfull + 8 * S, vfull = kempty + 8 * S,
+                   vempty = vfull + 8 * S, mfull = vempty + 8 * S, sfull = mfull + 8 * S,
+                   sfree = sfull + 16, pready = sfree + 16, pvdone = pready + 16,
+                   qfull = pvdone + 16, qempty = qfull + 8 * QB, ofree = qempty + 8 * QB,
+                   xstat = ofree + 8, drain_s = xstat + 16, drain_o = drain_s + 8;
     const int hpc = p.hpc, sub_log2 = 2 - p.hpc_log2;   // 4 / hpc warps per head
-    const int nq = max(16, 2 * G * hpc);                // columns of S
     const int tt = 1 << p.tt_log2;
 
     if (tid == 0) {
-        for (int i = 0; i < S; ++i) {
-            ptx::mbar_init(kfull + 8 * i, 1);
-            ptx::mbar_init(vfull + 8 * i, 1);
-            ptx::mbar_init(empty + 8 * i, 1);
-        }
+        for (int i = 0; i < 5 * S; ++i)          // (stages: one arrival each)
+            ptx::mbar_init(bars + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(sfull + 8 * i, 1);
+            ptx::mbar_init(sfull + 8 * i, 2);    // the product, and the issuing warp
             ptx::mbar_init(sfree + 8 * i, 4);
             ptx::mbar_init(pready + 8 * i, 4);
             ptx::mbar_init(pvdone + 8 * i, 1);
         }
         for (int i = 0; i < QB; ++i) {
             ptx::mbar_init(qfull + 8 * i, 2);
-            ptx::mbar_init(qempty + 8 * i, 5);   // the last S of the segment, softmax warps
+            ptx::mbar_init(qempty + 8 * i, 1);
         }
-        ptx::mbar_init(drain, 1);
+        ptx::mbar_init(ofree, 4);
+        ptx::mbar_init(xstat, 4);
+        ptx::mbar_init(xstat + 8, 4);
+        ptx::mbar_init(drain_s, 1);
+        ptx::mbar_init(drain_o, 1);
         *abort_flag = 0;
+        *tiles_done = 0;
+        *cut_s = make_int4(0, 0, 0, 0);
     }
     ptx::fence_mbar_init();
     // weight rows that no head fills stay zero
-    for (int i = tid; i < 2 * 4 * L::kP / 16; i += kQ8Threads)
+    for (int i = tid; i < 2 * 4 * L::kP / 16; i += L::kThreads)
         reinterpret_cast<uint4 *>(gen + L::p_off)[i] = make_uint4(0, 0, 0, 0);
     ptx::fence_proxy_async_smem();
-    if (warp == 4) {
+    if (warp == W_S) {
         ptx::tmem_alloc(ptx::smem_u32(tmem_holder), L::tmem_cols);
         ptx::tmem_relinquish();
     }
@@ -298,45 +323,70 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     const int C = min((int)gridDim.x, max(total, 1));
     const int R0 = q8_range_begin(blockIdx.x, C, total, p, cbase, lane);
     const int R1 = q8_range_begin(blockIdx.x + 1, C, total, p, cbase, lane);
+    const int nk = R1 - R0;
     if (tid == 0)
         ptx::grid_launch_dependents();
     const uint64_t lim = p.wait_ns;
+    // Whole warp: true once the phase is complete; false when another warp has
+    // given up or the bounded wait ran out.
+    auto ready = [&](uint32_t bar, uint32_t parity) -> bool {
+        if (__all_sync(kFull, ptx::mbar_test_wait(bar, parity)))
+            return true;
+        if (__any_sync(kFull, *abort_flag != 0))
+            return false;
+        return __all_sync(kFull, ptx::mbar_wait_bounded(bar, parity, lim));
+    };
+    auto give_up = [&]() {
+        if (lane == 0) {
+            report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
+            *abort_flag = 1;
+        }
+        __syncwarp();
+    };
 
-    if (warp == 5) {
+    if (warp == W_K || warp == W_V) {
         // ============================================== TMA and block scales
-        // Lane l serves box l % 8 (rows 16 (l % 8) ..: 16 tokens of one head)
-        // of tile l / 8 of a batch of four tiles; a batch's block ids are
-        // fetched one batch ahead.
-        const int box = lane & 7, slot = lane >> 3;
-        const int bw = box >> 1;                        // the box's softmax warp
+        // A tile of K (or V) comes as boxes of 16 or 32 tokens of one head.
+        // Lane l serves box l % nb of tile l / nb of a batch of 32 / nb tiles;
+        // a batch's block ids are fetched one batch ahead.
+        const bool is_k = warp == W_K;
+        const int nb_log2 = 7 - p.box_log2, nb = 1 << nb_log2;
+        const int box = lane & (nb - 1), slot = lane >> nb_log2, batch = 32 >> nb_log2;
+        const int row0 = box << p.box_log2;              // first row of the box in the tile
+        const int bw = row0 >> 5;                        // its softmax warp
         const int bhead = bw >> sub_log2;
-        const int btok = ((bw & ((1 << sub_log2) - 1)) << 5) + ((box & 1) << 4);
+        const int btok = ((bw & ((1 << sub_log2) - 1)) << 5) + (row0 & 31);
+        const uint32_t full = is_k ? kfull : vfull, empty = is_k ? kempty : vempty;
+        const void *tmap = is_k ? static_cast<const void *>(&tmap_k)
+                                : static_cast<const void *>(&tmap_v);
         struct Batch {
-            int b, hg, j, ns, n, id;
+            int b, hg, j, ns, n, seg, id;
             bool active;
         };
         bool ok = true;
-        int issued = R0;
-        if (R0 < R1) {
-            if (lane == 0) {
-                ptx::prefetch_tensormap(&tmap_k);
-                ptx::prefetch_tensormap(&tmap_v);
-            }
+        int issued = 0;
+        if (nk > 0) {
+            if (lane == 0)
+                ptx::prefetch_tensormap(tmap);
             const uint64_t policy = ptx::policy_evict_first();
             Q8Walk w = q8_walk_at(R0, p, cbase, lane);
+            int seg = 0;
             auto fill = [&](int g) {
-                Batch d = {0, 0, 0, 1, 0, -1, false};
+                Batch d = {0, 0, 0, 1, 0, 0, -1, false};
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < batch; ++i) {
                     if (g + i >= R1)
                         break;
-                    if (g + i >= w.g0 + w.nt)
+                    if (g + i >= w.g0 + w.nt) {
                         q8_walk_next(w, p, lane);
+                        ++seg;
+                    }
                     if (slot == i) {
                         d.b = w.b;
                         d.hg = w.hg;
                         d.j = g + i - w.g0;
                         d.ns = w.nt;
+                        d.seg = seg;
                         const int t0 = d.j << p.tt_log2;
                         d.n = min(tt, w.ctx - t0);
                         d.active = btok < d.n;
@@ -347,23 +397,22 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 }
                 return d;
             };
-            Batch cur = fill(R0), nxt = cur;
+            Batch cur = fill(R0), nxt;
             // pools and scales may be written by the kernel ahead
             ptx::grid_wait_prerequisites();
-            for (int g = R0; ok && g < R1; g += 4, cur = nxt) {
+            for (int k0 = 0; ok && k0 < nk; k0 += batch, cur = nxt) {
                 const bool valid = cur.active && cur.id >= 0 && (int64_t)cur.id < p.num_blocks;
                 const int head = cur.hg * hpc + bhead;
                 float ks = 0.f, vs = 0.f;
-                if (valid) {
+                if (valid && !is_k) {
                     const int64_t at = (int64_t)cur.id * p.num_kv_heads + head;
                     ks = __ldcg(p.k_scales + at);
                     vs = __ldcg(p.v_scales + at);
                 }
                 const unsigned vmask = __ballot_sync(kFull, valid);
                 const unsigned bmask = __ballot_sync(kFull, cur.active && !valid);
-                nxt = fill(g + 4);
-                for (int i = 0; i < 4 && g + i < R1; ++i) {
-                    const int k = g + i - R0, s = k % S;
+                for (int i = 0; i < batch && k0 + i < nk; ++i) {
+                    const int k = k0 + i, s = k % S;
                     if (__any_sync(kFull, *abort_flag != 0))
                         break;
                     if (k >= S &&
@@ -375,112 +424,76 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     }
                     // test hook: this CTA's second tile is never copied
                     const bool withhold = (int)blockIdx.x == p.withhold_cta && k == 1;
-                    const unsigned mine = (vmask >> (8 * i)) & 0xffu;
-                    const int from = 8 * i;
-                    const int mb = __shfl_sync(kFull, cur.b, from);
-                    const int mhg = __shfl_sync(kFull, cur.hg, from);
-                    const int mj = __shfl_sync(kFull, cur.j, from);
-                    const int mns = __shfl_sync(kFull, cur.ns, from);
-                    const int mn = __shfl_sync(kFull, cur.n, from);
-                    if (lane == 0) {
-                        Q8Meta &m = meta[s];
-                        m.b = mb;
-                        m.hg = mhg;
-                        m.j = mj;
-                        m.ns = mns;
-                        m.n = mn;
-                        m.first = mj == 0 || k == 0;
-                        m.last = mj == mns - 1 || g + i == R1 - 1;
-                        m.bad = ((bmask >> (8 * i)) & 0xffu) != 0;
-                        const uint32_t tx = (uint32_t)(__popc(mine) * 16 * D);
-                        ptx::mbar_expect_tx(kfull + 8 * s, tx);
-                        ptx::mbar_expect_tx(vfull + 8 * s, tx);
-                    }
+                    const int mine = __popc((vmask >> (i << nb_log2)) & ((1u << nb) - 1));
+                    if (lane == 0)
+                        ptx::mbar_expect_tx(full + 8 * s, (uint32_t)(mine << p.box_log2) * D);
                     __syncwarp();
-                    if (slot == i) {
-                        if (valid && !withhold) {
-                            const int t0 = (cur.j << p.tt_log2) + btok;
-                            const int row = cur.id * p.block_size + (t0 & (p.block_size - 1));
-                            const uint32_t dst = base + (uint32_t)(s * L::kStage + box * 16 * D);
-                            ptx::tma_load_5d(dst, &tmap_k, 0, 0, 0, row >> 3, head, kfull + 8 * s,
-                                             policy);
-                            ptx::tma_load_5d(dst + kQ8Tile * D, &tmap_v, 0, 0, 0, row >> 3, head,
-                                             vfull + 8 * s, policy);
+                    if (slot == i && valid && !withhold) {
+                        const int t0 = (cur.j << p.tt_log2) + btok;
+                        const int row = cur.id * p.block_size + (t0 & (p.block_size - 1));
+                        ptx::tma_load_5d(base + (uint32_t)((is_k ? 0 : L::v_off) + s * L::kStage +
+                                                           row0 * D),
+                                         tmap, 0, 0, 0, row >> 3, head, full + 8 * s, policy);
+                    }
+                    if (is_k) {
+                        if (slot == i && box == 0)
+                            kflag[s] = (cur.j == 0 || k == 0 ? 1 : 0) |
+                                       (cur.j == cur.ns - 1 || k == nk - 1 ? 2 : 0);
+                    } else {
+                        if (slot == i) {
+                            Q8Meta &m = meta[s];
+                            if (box == 0) {
+                                m.b = cur.b;
+                                m.hg = cur.hg;
+                                m.j = cur.j;
+                                m.ns = cur.ns;
+                                m.n = cur.n;
+                                m.seg = cur.seg;
+                                m.bad = ((bmask >> (i << nb_log2)) & ((1u << nb) - 1)) != 0;
+                            }
+                            m.ks[row0 >> 4] = ks;
+                            m.vs[row0 >> 4] = vs;
+                            if (p.box_log2 == 5) {
+                                m.ks[(row0 >> 4) + 1] = ks;
+                                m.vs[(row0 >> 4) + 1] = vs;
+                            }
                         }
-                        meta[s].ks[box] = ks;
-                        meta[s].vs[box] = vs;
                     }
                     __syncwarp();
-                    // (the arrivals release the metadata and the scales)
+                    // (the arrivals release the flags, the metadata and the scales)
                     if (lane == 0) {
-                        ptx::mbar_arrive(kfull + 8 * s);
-                        ptx::mbar_arrive(vfull + 8 * s);
+                        if (!is_k)
+                            ptx::mbar_arrive(mfull + 8 * s);
+                        ptx::mbar_arrive(full + 8 * s);
                     }
-                    issued = g + i + 1;
+                    issued = k + 1;
+                    if (i == 0)
+                        nxt = fill(R0 + k0 + batch);
                 }
-                if (issued < min(g + 4, R1))
+                if (issued < min(k0 + batch, nk))
                     break;
             }
         }
-        if (!ok && lane == 0) {
-            report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
-            *abort_flag = 1;
-        }
-        if (issued < R1) {
+        if (!ok)
+            give_up();
+        if (issued < nk) {
             // given up: let the copies in flight land before the CTA ends
-            for (int k = max(0, issued - R0 - S); k < issued - R0; ++k) {
-                ptx::mbar_wait_bounded(kfull + 8 * (k % S), (uint32_t)((k / S) & 1), lim);
-                ptx::mbar_wait_bounded(vfull + 8 * (k % S), (uint32_t)((k / S) & 1), lim);
-            }
+            for (int k = max(0, issued - S); k < issued; ++k)
+                ptx::mbar_wait_bounded(full + 8 * (k % S), (uint32_t)((k / S) & 1), lim);
         }
         __syncwarp();
-    } else if (warp == 4) {
-        // ======================================================= MMA issue
-        auto ready = [&](uint32_t bar, uint32_t parity) -> bool {
-            if (__all_sync(kFull, ptx::mbar_test_wait(bar, parity)))
-                return true;
-            if (__any_sync(kFull, *abort_flag != 0))
-                return false;
-            return __all_sync(kFull, ptx::mbar_wait_bounded(bar, parity, lim));
-        };
-        const uint32_t idesc_s = ptx::umma_idesc_f8(128, nq, false, false, false, false);
-        constexpr uint32_t idesc_o = ptx::umma_idesc_f8(128, NP, false, true, true, false);
+    } else if (warp == W_S) {
+        // ============================================================== S
+        const uint32_t idesc = ptx::umma_idesc_f8(128, max(16, 2 * G * hpc), false, false, false,
+                                                  false);
         bool ok = true;
         int seg = 0;
-        int fresh_prev = 0;
-        auto issue_pv = [&](int k, int fresh) -> bool {
-            const int s = k % S;
-            if (!ready(pready + 8 * (k & 1), (uint32_t)((k >> 1) & 1)) ||
-                !ready(vfull + 8 * s, (uint32_t)((k / S) & 1)))
-                return false;
-            ptx::tc_fence_after();
-            const uint32_t vst = base + (uint32_t)(s * L::kStage + kQ8Tile * D);
-            const uint32_t pst = base + (uint32_t)(L::p_off + (k & 1) * 4 * L::kP);
-            if (ptx::elect_one()) {
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint64_t bd = ptx::umma_desc_plain(pst + w * L::kP, 128, 256);
-#pragma unroll
-                    for (int h = 0; h < HALVES; ++h)
-                        ptx::umma_f8_ss(o_tm + (uint32_t)((w * HALVES + h) * NP),
-                                        ptx::umma_desc_sw128(vst + w * 32 * D + h * 1024, 1024,
-                                                             GROUP),
-                                        bd, idesc_o, fresh == 0);
-                }
-                ptx::umma_commit(empty + 8 * s);
-                ptx::umma_commit(pvdone + 8 * (k & 1));
-            }
-            __syncwarp();
-            return true;
-        };
-        const int nk = R1 - R0;
         for (int k = 0; k < nk; ++k) {
-            const int s = k % S;
+            const int s = k % S, qb = seg % QB;
             if (!(ok = ready(kfull + 8 * s, (uint32_t)((k / S) & 1))))
                 break;
-            const int first = meta[s].first, last = meta[s].last;
-            const int qb = seg % QB;
-            if (first && !(ok = ready(qfull + 8 * qb, (uint32_t)((seg / QB) & 1))))
+            const int flags = kflag[s];
+            if ((flags & 1) && !(ok = ready(qfull + 8 * qb, (uint32_t)((seg / QB) & 1))))
                 break;
             if (k >= 2 && !(ok = ready(sfree + 8 * (k & 1), (uint32_t)(((k >> 1) - 1) & 1))))
                 break;
@@ -492,34 +505,74 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
 #pragma unroll
                 for (int kk = 0; kk < D / 32; ++kk) {
                     const uint64_t off = (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
-                    ptx::umma_f8_ss(tmem + (uint32_t)((k & 1) * 64), ad + off, bd + off, idesc_s,
+                    ptx::umma_f8_ss(tmem + (uint32_t)((k & 1) * 64), ad + off, bd + off, idesc,
                                     kk > 0);
                 }
                 ptx::umma_commit(sfull + 8 * (k & 1));
-                if (last)
+                ptx::umma_commit(kempty + 8 * s);
+                if (flags & 2)
                     ptx::umma_commit(qempty + 8 * qb);
+                // (passes on the query factors, seen with qfull)
+                ptx::mbar_arrive(sfull + 8 * (k & 1));
             }
             __syncwarp();
-            seg += last;
-            if (k >= 1 && !(ok = issue_pv(k - 1, fresh_prev)))
-                break;
-            fresh_prev = first;
+            seg += flags >> 1;
         }
-        if (ok && nk > 0)
-            ok = issue_pv(nk - 1, fresh_prev);
         if (!ok) {
-            if (lane == 0) {
-                report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
-                *abort_flag = 1;
-            }
+            give_up();
             // products already issued finish before the memory goes
             if (ptx::elect_one())
-                ptx::umma_commit(drain);
+                ptx::umma_commit(drain_s);
             __syncwarp();
-            ptx::mbar_wait_bounded(drain, 0, lim);
+            ptx::mbar_wait_bounded(drain_s, 0, lim);
         }
         __syncwarp();
-    } else if (warp >= 6) {
+    } else if (warp == W_O) {
+        // ============================================================ O^T
+        constexpr uint32_t idesc = ptx::umma_idesc_f8(128, NP, false, true, true, false);
+        bool ok = true;
+        for (int k = 0; k < nk; ++k) {
+            const int s = k % S;
+            if (!(ok = ready(mfull + 8 * s, (uint32_t)((k / S) & 1))))
+                break;
+            const int j = meta[s].j, seg = meta[s].seg;
+            // a new segment: the epilogue of the one before has read O
+            if ((j == 0 || k == 0) && seg > 0 &&
+                !(ok = ready(ofree, (uint32_t)((seg - 1) & 1))))
+                break;
+            if (!(ok = ready(vfull + 8 * s, (uint32_t)((k / S) & 1)) &&
+                       ready(pready + 8 * (k & 1), (uint32_t)((k >> 1) & 1))))
+                break;
+            ptx::tc_fence_after();
+            const uint32_t vst = base + (uint32_t)(L::v_off + s * L::kStage);
+            const uint32_t pst = base + (uint32_t)(L::p_off + (k & 1) * 4 * L::kP);
+            const uint32_t acc = o_tm + (uint32_t)((k % SETS) * L::o_cols);
+            const bool add = j >= SETS && k >= SETS;     // not the set's first tile
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint64_t bd = ptx::umma_desc_plain(pst + w * L::kP, 128, 256);
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h)
+                        ptx::umma_f8_ss(acc + (uint32_t)((w * HALVES + h) * NP),
+                                        ptx::umma_desc_sw128(vst + w * 32 * D + h * 1024, 1024,
+                                                             GROUP),
+                                        bd, idesc, add);
+                }
+                ptx::umma_commit(vempty + 8 * s);
+                ptx::umma_commit(pvdone + 8 * (k & 1));
+            }
+            __syncwarp();
+        }
+        if (!ok) {
+            give_up();
+            if (ptx::elect_one())
+                ptx::umma_commit(drain_o);
+            __syncwarp();
+            ptx::mbar_wait_bounded(drain_o, 0, lim);
+        }
+        __syncwarp();
+    } else if (warp >= W_Q) {
         // ====================================================== query rows
         // Row (h, g) of a segment is scaled by a power of two (largest
         // element in [128, 256)) and split into hi = e4m3(y) and
@@ -527,7 +580,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         // rows (2 h) G + g and (2 h + 1) G + g of the B operand.
         ptx::grid_wait_prerequisites();
         bool ok = true;
-        if (R0 < R1) {
+        if (nk > 0) {
             constexpr int E = D / 32;                    // elements per lane
             Q8Walk w = q8_walk_at(R0, p, cbase, lane);
             for (int seg = 0; w.g0 < R1; ++seg) {
@@ -538,88 +591,103 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 const __nv_bfloat16 *src = p.q + ((int64_t)w.b * p.num_q_heads +
                                                   (int64_t)w.hg * rows) * D;
                 constexpr int RW = 4 * G / 2;            // rows per warp, at most
-                uint32_t x[RW][E / 2];
+                constexpr int RB = RW < 8 ? RW : 8;      // rows loaded at once
+                bool free = seg < QB;
+#pragma unroll 1
+                for (int r0 = 0; r0 < RW; r0 += RB) {
+                    uint32_t x[RB][E / 2];
 #pragma unroll
-                for (int i = 0; i < RW; ++i) {
-                    const int r = 2 * i + (warp - 6);
+                    for (int i = 0; i < RB; ++i) {
+                        const int r = 2 * (r0 + i) + (warp - W_Q);
 #pragma unroll
-                    for (int e = 0; e < E / 2; ++e)
-                        x[i][e] = 0;
-                    if (r < rows) {
+                        for (int e = 0; e < E / 2; ++e)
+                            x[i][e] = 0;
+                        if (r < rows) {
+                            if constexpr (E == 8) {
+                                const uint4 v = __ldg(
+                                    reinterpret_cast<const uint4 *>(src + (int64_t)r * D) + lane);
+                                x[i][0] = v.x;
+                                x[i][1] = v.y;
+                                x[i][2] = v.z;
+                                x[i][3] = v.w;
+                            } else {
+                                const uint2 v = __ldg(
+                                    reinterpret_cast<const uint2 *>(src + (int64_t)r * D) + lane);
+                                x[i][0] = v.x;
+                                x[i][1] = v.y;
+                            }
+                        }
+                    }
+                    if (!free) {
+                        if (!__all_sync(kFull, ptx::mbar_wait_bounded(
+                                                   qempty + 8 * qb,
+                                                   (uint32_t)((seg / QB - 1) & 1), lim))) {
+                            ok = false;
+                            break;
+                        }
+                        free = true;
+                    }
+                    const uint32_t qst = base + (uint32_t)(L::q_off + qb * L::kQRows * D);
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) {
+                        const int r = 2 * (r0 + i) + (warp - W_Q);
+                        if (r >= rows)
+                            continue;
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int e = 0; e < E / 2; ++e)
+                            top = max(top, max(x[i][e] << 16 & 0x7fffffffu, x[i][e] & 0x7fff0000u));
+                        top = __reduce_max_sync(kFull, top);
+                        const int ef = (int)(top >> 23);
+                        const float sigma = __uint_as_float((uint32_t)min(254, 261 - ef) << 23);
+                        uint32_t hi[E / 4], lo[E / 4];
+#pragma unroll
+                        for (int e = 0; e < E / 4; ++e) {
+                            uint32_t h2[2], l2[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float y0 = ptx::bf16lo_to_f32(x[i][2 * e + k]) * sigma;
+                                const float y1 = ptx::bf16hi_to_f32(x[i][2 * e + k]) * sigma;
+                                h2[k] = f32x2_to_e4m3x2(y0, y1);
+                                const uint32_t f = e4m3x2_to_f16x2(h2[k]);
+                                l2[k] = f32x2_to_e4m3x2(y0 - ptx::f16lo_to_f32(f),
+                                                        y1 - ptx::f16hi_to_f32(f));
+                            }
+                            hi[e] = h2[0] | (h2[1] << 16);
+                            lo[e] = l2[0] | (l2[1] << 16);
+                        }
+                        const int h = r / G, g = r - h * G;
+                        const int byte = lane * E;       // within the row
+                        auto at = [&](int n) {
+                            return qst + (uint32_t)((n >> 3) * GROUP + (byte >> 7) * 1024 +
+                                                    (n & 7) * 128 +
+                                                    ((((byte & 127) >> 4) ^ (n & 7)) << 4) +
+                                                    (byte & 15));
+                        };
+                        const uint32_t ah = at(2 * h * G + g), al = at((2 * h + 1) * G + g);
                         if constexpr (E == 8) {
-                            const uint4 v = __ldg(
-                                reinterpret_cast<const uint4 *>(src + (int64_t)r * D) + lane);
-                            x[i][0] = v.x;
-                            x[i][1] = v.y;
-                            x[i][2] = v.z;
-                            x[i][3] = v.w;
+                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(ah), "r"(hi[0]),
+                                         "r"(hi[E / 4 - 1])
+                                         : "memory");
+                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(al), "r"(lo[0]),
+                                         "r"(lo[E / 4 - 1])
+                                         : "memory");
                         } else {
-                            const uint2 v = __ldg(
-                                reinterpret_cast<const uint2 *>(src + (int64_t)r * D) + lane);
-                            x[i][0] = v.x;
-                            x[i][1] = v.y;
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(ah), "r"(hi[0]) : "memory");
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(al), "r"(lo[0]) : "memory");
                         }
+                        // A row with a non-finite element gives NaN logits.
+                        // (Four segments' factors are kept: the buffer of
+                        // segment seg is free, so S of an earlier one's last
+                        // tile is done, and every tile but the two before it
+                        // has been read with its factors.)
+                        if (lane == 0)
+                            sf[(seg & 3) * 4 * G + r] = ef < 255 ? p.scale_log2 / sigma
+                                                                 : __int_as_float(0x7fc00000);
                     }
                 }
-                if (seg >= QB &&
-                    !__all_sync(kFull, ptx::mbar_wait_bounded(qempty + 8 * qb,
-                                                              (uint32_t)((seg / QB - 1) & 1),
-                                                              lim))) {
-                    ok = false;
+                if (!ok)
                     break;
-                }
-                const uint32_t qst = base + (uint32_t)(L::q_off + qb * L::kQRows * D);
-#pragma unroll
-                for (int i = 0; i < RW; ++i) {
-                    const int r = 2 * i + (warp - 6);
-                    if (r >= rows)
-                        continue;
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int e = 0; e < E / 2; ++e)
-                        top = max(top, max(x[i][e] << 16 & 0x7fffffffu, x[i][e] & 0x7fff0000u));
-                    top = __reduce_max_sync(kFull, top);
-                    const int ef = (int)(top >> 23);
-                    const float sigma = __uint_as_float((uint32_t)min(254, 261 - ef) << 23);
-                    uint32_t hi[E / 4], lo[E / 4];
-#pragma unroll
-                    for (int e = 0; e < E / 4; ++e) {
-                        uint32_t h2[2], l2[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float y0 = ptx::bf16lo_to_f32(x[i][2 * e + k]) * sigma;
-                            const float y1 = ptx::bf16hi_to_f32(x[i][2 * e + k]) * sigma;
-                            h2[k] = f32x2_to_e4m3x2(y0, y1);
-                            const uint32_t f = e4m3x2_to_f16x2(h2[k]);
-                            l2[k] = f32x2_to_e4m3x2(y0 - ptx::f16lo_to_f32(f),
-                                                    y1 - ptx::f16hi_to_f32(f));
-                        }
-                        hi[e] = h2[0] | (h2[1] << 16);
-                        lo[e] = l2[0] | (l2[1] << 16);
-                    }
-                    const int h = r / G, g = r - h * G;
-                    const int byte = lane * E;           // within the row
-                    auto at = [&](int n) {
-                        return qst + (uint32_t)((n >> 3) * GROUP + (byte >> 7) * 1024 + (n & 7) * 128 +
-                                                ((((byte & 127) >> 4) ^ (n & 7)) << 4) + (byte & 15));
-                    };
-                    const uint32_t ah = at(2 * h * G + g), al = at((2 * h + 1) * G + g);
-                    if constexpr (E == 8) {
-                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(ah), "r"(hi[0]),
-                                     "r"(hi[E / 4 - 1])
-                                     : "memory");
-                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(al), "r"(lo[0]),
-                                     "r"(lo[E / 4 - 1])
-                                     : "memory");
-                    } else {
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(ah), "r"(hi[0]) : "memory");
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(al), "r"(lo[0]) : "memory");
-                    }
-                    // a row with a non-finite element gives NaN logits
-                    if (lane == 0)
-                        sf[qb * 4 * G + r] = ef < 255 ? p.scale_log2 / sigma
-                                                      : __int_as_float(0x7fc00000);
-                }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
@@ -629,20 +697,15 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 q8_walk_next(w, p, lane);
             }
         }
-        if (!ok && lane == 0) {
-            report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
-            *abort_flag = 1;
-        }
-        __syncwarp();
+        if (!ok)
+            give_up();
     } else {
         // ================================================ softmax, epilogue
+        const int set = warp >> 2, w4 = warp & 3, st = tid & 127;
+        const int rows = hpc * G;
         // outputs and the workspace may be in use by the kernel ahead
         ptx::grid_wait_prerequisites();
-        const int rows = hpc * G;
-        // until a piece of a segment that starts in this range says otherwise
-        if (p.mode == 0 && tid == 0)
-            p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
-        for (int b = blockIdx.x; b < p.num_seqs; b += gridDim.x) {
+        for (int b = blockIdx.x; set == 0 && b < p.num_seqs; b += gridDim.x) {
             const int len = p.context_lens[b];
             if (eff_ctx(len, p.ctx_cap) > 0)
                 continue;
@@ -652,109 +715,149 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             for (int i = tid; i < p.num_q_heads * D / 2; i += 128)
                 o[i] = 0;
         }
-        const int hl = warp >> sub_log2;                  // this warp's head of the group
-        const int tok = ((warp & ((1 << sub_log2) - 1)) << 5) + lane;
-        const int tok0 = tok - lane;
-        const uint32_t lane_tm = (uint32_t)(warp * 32) << 16;
-        const int nk = R1 - R0;
+        const int hl = w4 >> sub_log2;                    // this warp's head of the group
+        const int tok0 = (w4 & ((1 << sub_log2) - 1)) << 5, tok = tok0 + lane;
+        const uint32_t lane_tm = (uint32_t)(w4 * 32) << 16;
+        const uint32_t acc_tm = o_tm + (uint32_t)(set * L::o_cols) + lane_tm;
+        const int bar0 = 1 + 2 * set;
         float m[G], l[G], fac[G];
         bool fail = false, seg_bad = false;
-        int seg = 0, stop = nk;
+        int exchanges = 0;
         auto wait = [&](uint32_t bar, uint32_t parity) {
-            if (fail || __all_sync(kFull, ptx::mbar_test_wait(bar, parity)))
-                return;
-            if (__any_sync(kFull, *abort_flag != 0) ||
-                !__all_sync(kFull, ptx::mbar_wait_bounded(bar, parity, lim))) {
+            if (!fail && !ready(bar, parity)) {
                 fail = true;
-                if (lane == 0) {
-                    report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
-                    *abort_flag = 1;
-                }
-                __syncwarp();
+                give_up();
             }
         };
-        // Each iteration holds a barrier of the four warps, also for a warp
-        // whose wait ran out; only what the barrier says ends the loop, so that
-        // all four leave it together.
-        for (int k = 0; k < nk; ++k) {
+        // Each iteration holds a barrier of the set's four warps, also for a
+        // warp whose wait ran out; only what a barrier says ends the loop, so
+        // that all four leave it together.
+        for (int k = set; k < nk; k += SETS) {
             const int s = k % S;
-            const uint32_t s_tm = tmem + (uint32_t)((k & 1) * 64) + lane_tm;
             wait(sfull + 8 * (k & 1), (uint32_t)((k >> 1) & 1));
-            wait(kfull + 8 * s, (uint32_t)((k / S) & 1));  // (complete: for the metadata)
-            const int qb = seg % QB;
-            bool first = false, last = false, grow = false;
-            int n = 0;
-            float e[G], x[G];
+            wait(mfull + 8 * s, (uint32_t)((k / S) & 1));
+            bool first = false, over = false;
+            int n = 0, j = 0, seg = 0;
+            float t[G], lv = 0.f, vs = 0.f;
             if (!fail) {
-                first = meta[s].first;
-                last = meta[s].last;
                 n = meta[s].n;
+                j = meta[s].j;
+                seg = meta[s].seg;
+                const int box = 2 * w4 + (lane >> 4);
+                const float ks = meta[s].ks[box];
+                vs = meta[s].vs[box];
+                first = j < SETS || k < SETS;
                 if (first) {
-                    wait(qfull + 8 * qb, (uint32_t)((seg / QB) & 1));
                     seg_bad = false;
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
-                        m[g] = -INFINITY;
+                        fac[g] = sf[(seg & 3) * 4 * G + hl * G + g];
                         l[g] = 0.f;
-                        fac[g] = sf[qb * 4 * G + hl * G + g];
                     }
-                    __syncwarp();
-                    if (!fail && lane == 0)
-                        ptx::mbar_arrive(qempty + 8 * qb);   // the factors are read
                 }
-                if (meta[s].bad)
-                    seg_bad = true;
-            }
-            if (!fail) {
+                seg_bad |= meta[s].bad != 0;
                 ptx::tc_fence_after();
                 uint32_t u[2 * G];
-                ptx::tmem_ld<2 * G>(s_tm + (uint32_t)(hl * 2 * G), u);
+                ptx::tmem_ld<2 * G>(tmem + (uint32_t)((k & 1) * 64 + hl * 2 * G) + lane_tm, u);
+                lv = fmaxf(ptx::lg2(vs), -64.f);
                 ptx::tmem_wait_ld();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0)
+                if (!fail && lane == 0)
                     ptx::mbar_arrive(sfree + 8 * (k & 1));
                 ptx::tmem_hold<2 * G>(u);
-                const int box = 2 * warp + (lane >> 4);
-                const float ks = meta[s].ks[box], vs = meta[s].vs[box];
-                const float lv = fmaxf(ptx::lg2(vs), -64.f);
                 const bool seen = tok < n;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     const float sg = (__uint_as_float(u[g]) + __uint_as_float(u[G + g])) *
                                      (fac[g] * ks);
-                    const float mx = ptx::warp_max(seen ? sg + lv : -INFINITY);
+                    t[g] = seen ? sg : -INFINITY;
+                }
+                if (first) {
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+                        m[g] = ptx::warp_max(t[g] + lv);
+                }
+                // (a warp without tokens so far has m = -inf: any token is over)
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    over |= t[g] + lv > m[g] + kQ8Grow;
+            }
+            if (ptx::barrier_or(bar0, 128, over || fail)) {
+                if (ptx::barrier_or(bar0 + 1, 128, fail))
+                    break;
+                // some lane of the set is past its reference: new references
+                bool scale_o = false;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float mx = ptx::warp_max(t[g] + lv);
                     float al = 1.f;
-                    if (m[g] == -INFINITY) {
-                        m[g] = mx;                        // nothing accumulated yet
-                    } else if (mx > m[g] + kQ8Grow) {
-                        al = ptx::ex2(m[g] - mx);
+                    if (mx > m[g] + kQ8Grow) {
+                        // (from -inf there is nothing to rescale)
+                        if (m[g] != -INFINITY) {
+                            al = ptx::ex2(m[g] - mx);
+                            scale_o = true;
+                        }
                         l[g] *= al;
                         m[g] = mx;
-                        grow = true;
                     }
                     if (lane == 0)
-                        alpha_s[((k & 1) * 4 + warp) * G + g] = al;
-                    e[g] = seen ? ptx::ex2(sg - m[g]) : 0.f;
-                    l[g] += e[g];
-                    x[g] = seen ? e[g] * (vs * kQ8Weight) : 0.f;
+                        alpha_s[(set * 4 + w4) * G + g] = al;
                 }
-            }
-            grow = ptx::barrier_or(1, 128, grow || fail);
-            if (grow && ptx::barrier_or(2, 128, fail)) {
-                fail = true;
-                stop = k;
-                break;
+                if (ptx::barrier_or(bar0, 128, scale_o)) {
+                    // the set's accumulators, once its product before is in
+                    wait(pvdone + 8 * ((k - SETS) & 1), (uint32_t)(((k - SETS) >> 1) & 1));
+                    ptx::tc_fence_after();
+#pragma unroll 1
+                    for (int w = 0; w < 4 && !fail; ++w) {
+                        float al[G];
+                        bool any = false;
+#pragma unroll
+                        for (int g = 0; g < G; ++g) {
+                            al[g] = alpha_s[(set * 4 + w) * G + g];
+                            any |= al[g] != 1.f;
+                        }
+                        if (!any)
+                            continue;
+#pragma unroll 1
+                        for (int c = 0; c < HALVES * (NP / 16); ++c) {
+                            const uint32_t at = acc_tm + (uint32_t)(w * HALVES * NP + c * 16);
+                            uint32_t u[16];
+                            ptx::tmem_ld16(at, u);
+                            ptx::tmem_wait_ld();
+                            ptx::tmem_hold16(u);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                u[i] = __float_as_uint(__uint_as_float(u[i]) *
+                                                       ((i & (GP - 1)) < G ? al[(i & (GP - 1)) % G]
+                                                                           : 1.f));
+                            ptx::tmem_st16(at, u);
+                        }
+                        ptx::tmem_wait_st();
+                    }
+                    ptx::tc_fence_before();
+                }
             }
             // weights of tile k - 2 have been used
             if (k >= 2)
                 wait(pvdone + 8 * (k & 1), (uint32_t)(((k >> 1) - 1) & 1));
+            const int nv = min(max(n - tok0, 0), 32);
+            if (nv < 32)
+                wait(vfull + 8 * s, (uint32_t)((k / S) & 1));
             if (!fail) {
-                const uint32_t pw = base + (uint32_t)(L::p_off + ((k & 1) * 4 + warp) * L::kP +
+                const uint32_t pw = base + (uint32_t)(L::p_off + ((k & 1) * 4 + w4) * L::kP +
                                                       (lane >> 4) * 128 + (lane & 15));
                 auto put = [&](int row, uint32_t v) {
                     st_shared_u8(pw + (uint32_t)((row >> 3) * 256 + (row & 7) * 16), v);
                 };
+                const float vw = vs * kQ8Weight;
+                float x[G];
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float e = lane < nv ? ptx::ex2(t[g] - m[g]) : 0.f;
+                    l[g] += e;
+                    x[g] = lane < nv ? e * vw : 0.f;
+                }
 #pragma unroll
                 for (int g = 0; g < G; g += 2) {
                     const float x0 = x[g], x1 = g + 1 < G ? x[g + 1 < G ? g + 1 : g] : 0.f;
@@ -774,14 +877,12 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                         put(2 * GP + g + 1, pc >> 8);
                     }
                 }
-                const int nv = min(max(n - tok0, 0), 32);
                 if (nv < 32) {
                     // V rows past the sequence hold whatever was there; their
                     // weight is 0, but 0 * NaN is NaN
-                    wait(vfull + 8 * s, (uint32_t)((k / S) & 1));
-                    const uint32_t vst =
-                        base + (uint32_t)(s * L::kStage + kQ8Tile * D + warp * 32 * D);
-                    for (int i = lane; i < (32 - nv) * (D / 16) && !fail; i += 32) {
+                    const uint32_t vst = base + (uint32_t)(L::v_off + s * L::kStage + w4 * 32 * D);
+#pragma unroll 1
+                    for (int i = lane; i < (32 - nv) * (D / 16); i += 32) {
                         const int r = nv + i / (D / 16), c = i % (D / 16);
                         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
                                          vst + (uint32_t)((r >> 3) * GROUP + (c >> 3) * 1024 +
@@ -792,90 +893,88 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 }
                 ptx::fence_proxy_async_smem();
             }
-            if (grow && !first) {
-                // every accumulator column by its head's factor, once the
-                // product of tile k - 1 is in
-                wait(pvdone + 8 * ((k + 1) & 1), (uint32_t)(((k - 1) >> 1) & 1));
-                if (!fail) {
-                    ptx::tc_fence_after();
-#pragma unroll 1
-                    for (int w = 0; w < 4; ++w) {
-                        float al[G];
-#pragma unroll
-                        for (int g = 0; g < G; ++g)
-                            al[g] = alpha_s[((k & 1) * 4 + w) * G + g];
-#pragma unroll 1
-                        for (int c = 0; c < HALVES * (NP / 16); ++c) {
-                            const uint32_t at =
-                                o_tm + lane_tm + (uint32_t)(w * HALVES * NP + c * 16);
-                            uint32_t u[16];
-                            ptx::tmem_ld16(at, u);
-                            ptx::tmem_wait_ld();
-                            ptx::tmem_hold16(u);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                u[i] = __float_as_uint(__uint_as_float(u[i]) *
-                                                       ((i & (GP - 1)) < G ? al[(i & (GP - 1)) % G]
-                                                                           : 1.f));
-                            ptx::tmem_st16(at, u);
-                        }
-                    }
-                    ptx::tmem_wait_st();
-                    ptx::tc_fence_before();
-                }
-            }
-            const bool cut_bad = seg_bad;
-            const Q8Meta &md = meta[s];
-            const int mb = md.b, mhg = md.hg, mj = md.j, mns = md.ns;
+            const int ns = meta[s].ns, mb = meta[s].b, mhg = meta[s].hg;
             __syncwarp();
             if (!fail && lane == 0)
                 ptx::mbar_arrive(pready + 8 * (k & 1));
-            seg += last;
-            if (!last)
+            // the set's last tile of the segment's share of this range?
+            const int left = min(ns - 1 - j, nk - 1 - k);     // tiles of the share after this
+            if (left >= SETS)
                 continue;
-            // ---- the segment's share of this range is complete
-            wait(pvdone + 8 * (k & 1), (uint32_t)((k >> 1) & 1));
+            const int share = min(j, k) + 1 + left;           // tiles of the share
+            float *my = stat + ((seg & 1) * SETS + set) * 4 * 2 * G;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1)
                     l[g] += __shfl_xor_sync(kFull, l[g], o);
                 if (lane == 0) {
-                    stat[(warp * 2) * G + g] = m[g];
-                    stat[(warp * 2 + 1) * G + g] = l[g];
+                    my[w4 * 2 * G + g] = m[g];
+                    my[w4 * 2 * G + G + g] = l[g];
                 }
             }
-            const bool any_fail = ptx::barrier_or(2, 128, fail);
-            if (any_fail) {
+            if (SETS > 1 && share > 1) {
+                // (two barriers in turn: a set may hand over once more before
+                // the other has taken the last one, but not twice, since its
+                // second tile from then needs the accumulators)
+                ++exchanges;
+                if (left > 0) {
+                    // the other set has the segment's last tile and joins both
+                    // (a bad block of this set's tiles: marked in its sums)
+                    if (seg_bad && lane == 0)
+                        my[w4 * 2 * G + G] = -1.f;
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive(xstat + 8 * (exchanges & 1));
+                    continue;
+                }
+                wait(xstat + 8 * (exchanges & 1), (uint32_t)(((exchanges - 1) >> 1) & 1));
+            }
+            // ---- the segment's share of this range is complete
+            wait(pvdone + 8 * (k & 1), (uint32_t)((k >> 1) & 1));
+            if (ptx::barrier_or(bar0, 128, fail)) {
                 fail = true;
-                stop = k;
                 break;
             }
             ptx::tc_fence_after();
-            const int segS = R0 + k - mj, segE = segS + mns;
+            const int segS = R0 + k - j, segE = segS + ns;
             const bool complete = segS >= R0 && segE <= R1;
             const bool piece_first = segS >= R0;
             float *ps = p.pieces + (int64_t)(2 * blockIdx.x + (piece_first ? 1 : 0)) * p.slot_floats;
-            const int subs = 1 << sub_log2;
-            if (cut_bad && complete && tid == 0)
-                report(p.dev_status, PA_DEV_BAD_BLOCK);
+            const int nsets = share > 1 ? SETS : 1, e0 = share > 1 ? 0 : set;
+            const float *both = stat + (seg & 1) * SETS * 4 * 2 * G;
+            // Factors of this warp's accumulators in each set, one head row
+            // per lane: 2^(m - M) over the row's sets and warps, over the sum
+            // when the segment is complete.
+            for (int e = e0; e < e0 + nsets; ++e)
+                for (int w = 0; w < 4; ++w)
+                    seg_bad |= both[(e * 4 + w) * 2 * G + G] == -1.f;
+            if (lane < G) {
+                const int w0 = hl << sub_log2;
+                float M = -INFINITY, sum = 0.f;
+                for (int e = e0; e < e0 + nsets; ++e)
+                    for (int w = w0; w < w0 + (1 << sub_log2); ++w)
+                        M = fmaxf(M, both[(e * 4 + w) * 2 * G + lane]);
+                for (int e = e0; e < e0 + nsets; ++e)
+                    for (int w = w0; w < w0 + (1 << sub_log2); ++w) {
+                        const float mw = both[(e * 4 + w) * 2 * G + lane];
+                        if (mw != -INFINITY)
+                            sum += both[(e * 4 + w) * 2 * G + G + lane] * ptx::ex2(mw - M);
+                    }
+                const float inv = !complete ? 1.f : (sum == 0.f ? 0.f : 1.f / (sum * kQ8Weight));
+                for (int e = e0; e < e0 + nsets; ++e) {
+                    const float mw = both[(e * 4 + w4) * 2 * G + lane];
+                    fac_s[(e * 4 + w4) * G + lane] = mw == -INFINITY ? 0.f : ptx::ex2(mw - M) * inv;
+                }
+                if (!complete && (w4 & ((1 << sub_log2) - 1)) == 0) {
+                    ps[rows * D + 2 * (hl * G + lane)] = M;
+                    ps[rows * D + 2 * (hl * G + lane) + 1] = sum;
+                }
+            }
+            if (ptx::barrier_or(bar0, 128, false))
+                break;                                        // (never: orders the factors)
 #pragma unroll 1
             for (int h = 0; h < hpc; ++h) {
-                // the head's warps joined: f = 2^(m_w - M), over the sum when
-                // the segment is complete (the weights' 2^11 cancels there)
-                float M[G], Lt[G];
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    M[g] = -INFINITY;
-                    for (int w = 0; w < subs; ++w)
-                        M[g] = fmaxf(M[g], stat[((h * subs + w) * 2) * G + g]);
-                    Lt[g] = 0.f;
-                    for (int w = 0; w < subs; ++w) {
-                        const float mw = stat[((h * subs + w) * 2) * G + g];
-                        if (mw != -INFINITY)
-                            Lt[g] += stat[((h * subs + w) * 2 + 1) * G + g] * ptx::ex2(mw - M[g]);
-                    }
-                }
                 float v[HALVES][G];
 #pragma unroll
                 for (int hf = 0; hf < HALVES; ++hf)
@@ -883,88 +982,97 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     for (int g = 0; g < G; ++g)
                         v[hf][g] = 0.f;
 #pragma unroll 1
-                for (int w = 0; w < subs; ++w) {
-                    const int vw = h * subs + w;
-                    float f[G];
+                for (int x = 0; x < nsets << sub_log2; ++x) {
+                    const int e = e0 + (x >> sub_log2);
+                    const int w = (h << sub_log2) + (x & ((1 << sub_log2) - 1));
+                    const uint32_t at = o_tm + lane_tm + (uint32_t)(e * L::o_cols + w * HALVES * NP);
+                    uint32_t u[HALVES][NP];
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        const float mw = stat[(vw * 2) * G + g];
-                        f[g] = mw == -INFINITY ? 0.f : ptx::ex2(mw - M[g]);
-                        if (complete)
-                            f[g] = Lt[g] > 0.f ? f[g] / Lt[g] : (Lt[g] == 0.f ? 0.f : Lt[g]);
-                    }
-#pragma unroll
-                    for (int hf = 0; hf < HALVES; ++hf) {
-                        uint32_t u[NP];
+                    for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
                         for (int c = 0; c < NP / 16; ++c)
-                            ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)((vw * HALVES + hf) * NP + 16 * c),
-                                           *reinterpret_cast<uint32_t(*)[16]>(&u[16 * c]));
-                        ptx::tmem_wait_ld();
-                        ptx::tmem_hold<NP>(u);
+                            ptx::tmem_ld16(at + (uint32_t)(hf * NP + 16 * c),
+                                           *reinterpret_cast<uint32_t(*)[16]>(&u[hf][16 * c]));
+                    float f[G];
 #pragma unroll
-                        for (int g = 0; g < G; ++g)
-                            v[hf][g] += f[g] * ((__uint_as_float(u[g]) + __uint_as_float(u[GP + g])) +
-                                                __uint_as_float(u[2 * GP + g]));
-                    }
-                }
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
+                    for (int g = 0; g < G; ++g)
+                        f[g] = fac_s[(e * 4 + w) * G + g];
+                    ptx::tmem_wait_ld();
 #pragma unroll
                     for (int hf = 0; hf < HALVES; ++hf) {
-                        const int d = hf * 128 + warp * 32 + lane;
-                        if (complete) {
-                            const float r = cut_bad ? 0.f : v[hf][g] * (1.f / kQ8Weight);
-                            p.out[((int64_t)mb * p.num_q_heads + (int64_t)mhg * rows + h * G + g) * D +
-                                  d] = __float2bfloat16_rn(r);
-                        } else {
-                            ps[(h * G + g) * D + d] = v[hf][g];
-                        }
-                    }
-                    if (!complete && tid == 0) {
-                        ps[rows * D + 2 * (h * G + g)] = M[g];
-                        ps[rows * D + 2 * (h * G + g) + 1] = Lt[g];
+                        ptx::tmem_hold<NP>(u[hf]);
+#pragma unroll
+                        for (int g = 0; g < G; ++g)
+                            v[hf][g] += f[g] * ((__uint_as_float(u[hf][g]) +
+                                                 __uint_as_float(u[hf][GP + g])) +
+                                                __uint_as_float(u[hf][2 * GP + g]));
                     }
                 }
+                if (complete) {
+                    __nv_bfloat16 *o = p.out + ((int64_t)mb * p.num_q_heads + (int64_t)mhg * rows +
+                                                h * G) * D + w4 * 32 + lane;
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+#pragma unroll
+                        for (int hf = 0; hf < HALVES; ++hf)
+                            o[g * D + hf * 128] = __float2bfloat16_rn(seg_bad ? 0.f : v[hf][g]);
+                } else {
+                    float *o = ps + h * G * D + w4 * 32 + lane;
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+#pragma unroll
+                        for (int hf = 0; hf < HALVES; ++hf)
+                            o[g * D + hf * 128] = v[hf][g];
+                }
             }
-            if (!complete && tid == 0) {
-                ps[rows * D + 2 * rows] = cut_bad ? 1.f : 0.f;
-                // the CTA in whose range the segment starts names it
-                if (piece_first)
-                    p.cuts[blockIdx.x] =
-                        make_int4(mb, mhg, cta_of(segE - 1, C, total) - (int)blockIdx.x + 1, 0);
+            if (st == 0) {
+                if (complete && seg_bad)
+                    report(p.dev_status, PA_DEV_BAD_BLOCK);
+                if (!complete) {
+                    ps[rows * D + 2 * rows] = seg_bad ? 1.f : 0.f;
+                    // the CTA in whose range the segment starts names it
+                    if (piece_first)
+                        *cut_s = make_int4(mb, mhg, cta_of(segE - 1, C, total) - (int)blockIdx.x + 1,
+                                           0);
+                }
+                *tiles_done = k + 1;
             }
+            // O may be overwritten
             ptx::tc_fence_before();
-        }
-        if (stop < nk) {
-            // a wait ran out: zeros for the segments from this tile on, and a
-            // mark in their pieces
-            Q8Walk w = q8_walk_at(R0 + stop, p, cbase, lane);
-            while (true) {
-                const int segE = w.g0 + w.nt;
-                if (w.g0 >= R0 && segE <= R1) {
-                    __nv_bfloat16 *o = p.out + ((int64_t)w.b * p.num_q_heads + (int64_t)w.hg * rows) * D;
-                    for (int i = tid; i < rows * D; i += 128)
-                        o[i] = __float2bfloat16_rn(0.f);
-                } else if (tid == 0) {
-                    float *ps = p.pieces +
-                                (int64_t)(2 * blockIdx.x + (w.g0 >= R0 ? 1 : 0)) * p.slot_floats;
-                    ps[rows * D + 2 * rows] = 2.f;
-                    if (w.g0 >= R0)
-                        p.cuts[blockIdx.x] =
-                            make_int4(w.b, w.hg, cta_of(segE - 1, C, total) - (int)blockIdx.x + 1, 0);
-                }
-                if (segE >= R1)
-                    break;
-                q8_walk_next(w, p, lane);
-            }
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(ofree);
         }
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == 4)
+    if (warp == W_S)
         ptx::tmem_dealloc(tmem, L::tmem_cols);
+    if (nk > 0 && *tiles_done < nk) {
+        // a wait ran out: zeros for the segments that are not complete, and a
+        // mark in their pieces
+        const int rows = hpc * G;
+        Q8Walk w = q8_walk_at(R0 + *tiles_done, p, cbase, lane);
+        while (true) {
+            const int segE = w.g0 + w.nt;
+            if (w.g0 >= R0 && segE <= R1) {
+                __nv_bfloat16 *o = p.out + ((int64_t)w.b * p.num_q_heads + (int64_t)w.hg * rows) * D;
+                for (int i = tid; i < rows * D; i += L::kThreads)
+                    o[i] = __float2bfloat16_rn(0.f);
+            } else if (tid == 0) {
+                float *ps = p.pieces + (int64_t)(2 * blockIdx.x + (w.g0 >= R0 ? 1 : 0)) * p.slot_floats;
+                ps[rows * D + 2 * rows] = 2.f;
+                if (w.g0 >= R0)
+                    *cut_s = make_int4(w.b, w.hg, cta_of(segE - 1, C, total) - (int)blockIdx.x + 1, 0);
+            }
+            if (segE >= R1)
+                break;
+            q8_walk_next(w, p, lane);
+        }
+    }
+    if (p.mode == 0 && tid == 0)
+        p.cuts[blockIdx.x] = *cut_s;
 }
 
 // Joins the pieces of every segment that range borders cut: CTA (x, head,

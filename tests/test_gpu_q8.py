@@ -135,8 +135,12 @@ def test_decode_long_contexts(pa, lens, hq, hkv, d, bs, workspace):
 
 def test_decode_many_short_sequences(pa):
     rng = np.random.default_rng(1)
-    c = Case(2, rng.integers(0, 90, 700), 8, 4, 128, 16)
-    c.check(c.decode(pa), False)
+    for hq, hkv, d, bs in ((8, 4, 128, 16), (16, 4, 256, 16), (32, 4, 256, 32), (8, 1, 128, 32)):
+        c = Case(2, rng.integers(0, 90, 700), hq, hkv, d, bs)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = c.decode(pa, status=status)
+        assert int(status.item()) == 0
+        c.check(out, False)
 
 
 @pytest.mark.parametrize("scale", [-0.06, 0.0, 3.0])
