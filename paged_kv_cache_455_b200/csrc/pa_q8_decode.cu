@@ -12,7 +12,8 @@ namespace {
 struct Launch {
     pa::Q8DecodeParams p;
     CUtensorMap tk, tv;
-    int grid;                // in: wanted, out: launched
+    int grid;
+    int chunks;              // 32-sequence chunks the prefix has room for
     void *stream;
 };
 
@@ -21,7 +22,7 @@ template <int D, int G>
 pa_status run(Launch &L, bool launch)
 {
     auto fn = &pa::q8_decode_kernel<D, G>;
-    constexpr int smem = pa::Q8Smem<D, G>::bytes;
+    const int smem = pa::Q8Smem<D, G>::bytes + 4 * (L.chunks + 1);
     int cap = 0;
     const pa_status st = pa::grid_capacity(reinterpret_cast<const void *>(fn), pa::Q8Smem<D, G>::kThreads,
                                            smem, &cap);
@@ -106,6 +107,9 @@ extern "C" pa_status pa_decode_attention_q8(void *out, const void *query, const 
     p.wait_ns = wait_ns ? wait_ns : pa::kWaitLimitNs;
     p.withhold_cta = pa::test_withhold_cta();
     L.stream = stream;
+    // (rounded up, so that few sizes occur)
+    for (L.chunks = 1; 32 * L.chunks < num_seqs;)
+        L.chunks *= 2;
     if (!pa::pool_map_grouped(&L.tk, k_pool, num_blocks, block_size, num_kv_heads, head_dim,
                               PA_DTYPE_FP8_E4M3, block_size) ||
         !pa::pool_map_grouped(&L.tv, v_pool, num_blocks, block_size, num_kv_heads, head_dim,
@@ -132,7 +136,8 @@ extern "C" pa_status pa_decode_attention_q8(void *out, const void *query, const 
     st = run_any(L, head_dim, group, true);
     if (st != PA_OK || !split)
         return st;
-    const int parts = std::max(1, group * head_dim / 512);
-    return pa::launch_dependent(pa::q8_merge_kernel, (unsigned)(L.grid * p.hpc * parts), 128, 0,
-                                stream, p, group, head_dim, parts);
+    const int parts = std::max(1, group * head_dim / (4 * pa::kQ8MergeThreads));
+    return pa::launch_dependent(pa::q8_merge_kernel, (unsigned)(L.grid * p.hpc * parts),
+                                pa::kQ8MergeThreads, (size_t)(L.grid * group) * 4, stream, p,
+                                group, head_dim, parts);
 }

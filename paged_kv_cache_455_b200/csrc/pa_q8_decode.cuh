@@ -19,16 +19,18 @@
 // so no code is ever converted or moved by a thread, and the softmax of one
 // tile is 32 tokens per warp, one per lane.
 //
-// Weights.  x_t = 2^7 vs(t) 2^(s_t - m) with m a running reference per head
-// and warp, raised to max_t (s_t + log2 vs(t)) whenever that has grown past
-// m + 8 (log2 units): x_t <= 2^15.  The three E5M2 parts are the value rounded
-// to 3 bits, the rest rounded to 3, and again: error 2^-9 of x_t down to
-// x_t = 2^-8 and 2^-17 below, that is 2^-24 of the largest weight, so that many
-// small weights next to a large one are not lost.  The row sums take the fp32
-// weights 2^(s_t - m).  Because m follows the weights with their scales, the
-// errors are relative to what the output is made of, whatever the scales'
-// spread.  A warp needs the maximum itself only for its first tile and when a
-// vote finds a lane past the reference, and accumulators are rescaled only then.
+// Weights.  x_t = vs(t) 2^(s_t - m) with m a running reference per head and
+// warp, raised to max_t (s_t + log2 vs(t)) whenever that has grown past m + 15
+// (log2 units): x_t <= 2^15.  The three E5M2 parts are the value rounded to 3
+// bits, the rest times 8 rounded to 3, and again; each part has accumulators of
+// its own, so the factors of 8 come out at the end and all parts have the
+// type's whole range: error 2^-9 of x_t down to x_t = 2^-14 and 2^-23 below,
+// relative to a largest weight of at least 1, so that many small weights next
+// to a large one are not lost.  The row sums take the fp32 weights 2^(s_t - m).
+// Because m follows the weights with their scales, the errors are relative to
+// what the output is made of, whatever the scales' spread.  A warp needs the
+// maximum itself only for its first tile and when a vote finds a lane past the
+// reference, and accumulators are rescaled only then.
 //
 // Warps: SETS x 4 softmax and epilogue, then one each for S, O^T, the TMA of K,
 // the TMA of V with the block scales, and two for the query rows.  The softmax
@@ -52,8 +54,7 @@ namespace pa {
 
 constexpr int kQ8Tile = 128;              // rows of K and V per tile (MMA M)
 constexpr int kQ8SmemStages = 6 * 32768;  // bytes of the stage ring
-constexpr float kQ8Grow = 8.f;            // log2 growth that makes a rescale
-constexpr float kQ8Weight = 128.f;        // 2^7: a weight at the reference
+constexpr float kQ8Grow = 15.f;           // log2 growth that makes a rescale
 
 struct Q8DecodeParams {
     __nv_bfloat16 *out;
@@ -61,7 +62,8 @@ struct Q8DecodeParams {
     const float *k_scales, *v_scales;
     const int32_t *block_tables, *context_lens;
     float *pieces;           // mode 0: two slots per CTA
-    int4 *cuts;              // mode 0: per CTA (sequence, head group, pieces or 0, -)
+    int4 *cuts;              // mode 0, per CTA: sequence, head group and pieces of the
+                             // segment that starts in its range and runs past it (0: none)
     int32_t *dev_status;
     int64_t num_blocks;
     int num_seqs, num_q_heads, num_kv_heads;
@@ -117,8 +119,9 @@ struct Q8Smem {
     static constexpr int kBars = 5 * kStages + 8 + 2 * kQBufs + 5;
     static constexpr int flag_off = bar_off + 8 * kBars;   // abort, tensor memory, tiles done
     static constexpr int cbase_off = flag_off + 16;
-    static constexpr int bytes = 1024 + cbase_off + 4 * (kMaxChunks + 1);
-    static_assert(bytes <= kSmemBudget, "shared memory per CTA");
+    // (the prefix of the tile counts comes last, as long as the batch needs)
+    static constexpr int bytes = 1024 + cbase_off;
+    static_assert(bytes + 4 * (kMaxChunks + 1) <= kSmemBudget, "shared memory per CTA");
 };
 
 // Position in the batch's sequence of segments (whole warp, uniform).
@@ -232,12 +235,7 @@ __device__ __forceinline__ int q8_range_begin(int x, int C, int T, const Q8Decod
     return w.g0 == g ? g : w.g0 + w.nt;
 }
 
-// x to the nearest value with three significant bits (E5M2's; x >= 0, finite).
-__device__ __forceinline__ float round3(float x)
-{
-    return __uint_as_float((__float_as_uint(x) + 0x100000u) & 0xffe00000u);
-}
-
+// Two fp32 values to E5M2 codes, `lo` in byte 0 (nearest, ties to even).
 __device__ __forceinline__ uint32_t e5m2x2(float lo, float hi)
 {
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
@@ -373,6 +371,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             int seg = 0;
             auto fill = [&](int g) {
                 Batch d = {0, 0, 0, 1, 0, 0, -1, false};
+                int t0 = 0;
 #pragma unroll 1
                 for (int i = 0; i < batch; ++i) {
                     if (g + i >= R1)
@@ -387,14 +386,15 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                         d.j = g + i - w.g0;
                         d.ns = w.nt;
                         d.seg = seg;
-                        const int t0 = d.j << p.tt_log2;
+                        t0 = d.j << p.tt_log2;
                         d.n = min(tt, w.ctx - t0);
                         d.active = btok < d.n;
-                        if (d.active)
-                            d.id = __ldg(p.block_tables + (int64_t)w.b * p.max_blocks +
-                                         ((t0 + btok) >> p.bs_log2));
                     }
                 }
+                // one load for the whole batch, waited for by its first use
+                if (d.active)
+                    d.id = __ldg(p.block_tables + (int64_t)d.b * p.max_blocks +
+                                 ((t0 + btok) >> p.bs_log2));
                 return d;
             };
             Batch cur = fill(R0), nxt;
@@ -850,31 +850,30 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                 auto put = [&](int row, uint32_t v) {
                     st_shared_u8(pw + (uint32_t)((row >> 3) * 256 + (row & 7) * 16), v);
                 };
-                const float vw = vs * kQ8Weight;
                 float x[G];
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     const float e = lane < nv ? ptx::ex2(t[g] - m[g]) : 0.f;
                     l[g] += e;
-                    x[g] = lane < nv ? e * vw : 0.f;
+                    x[g] = lane < nv ? e * vs : 0.f;
                 }
 #pragma unroll
                 for (int g = 0; g < G; g += 2) {
-                    const float x0 = x[g], x1 = g + 1 < G ? x[g + 1 < G ? g + 1 : g] : 0.f;
-                    const float a0 = round3(x0), a1 = round3(x1);
-                    const float b0 = x0 - a0, b1 = x1 - a1;
-                    const uint32_t pa0 = e5m2x2(a0, a1), pb = e5m2x2(b0, b1);
-                    const __half2_raw bh =
-                        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pb, __NV_E5M2);
-                    const uint32_t bf = (uint32_t)bh.x | ((uint32_t)bh.y << 16);
-                    const uint32_t pc = e5m2x2(b0 - ptx::f16lo_to_f32(bf), b1 - ptx::f16hi_to_f32(bf));
-                    put(g, pa0 & 0xffu);
-                    put(GP + g, pb & 0xffu);
-                    put(2 * GP + g, pc & 0xffu);
-                    if (g + 1 < G) {
-                        put(g + 1, pa0 >> 8);
-                        put(GP + g + 1, pb >> 8);
-                        put(2 * GP + g + 1, pc >> 8);
+                    float x0 = x[g], x1 = g + 1 < G ? x[g + 1 < G ? g + 1 : g] : 0.f;
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {
+                        const uint32_t c = e5m2x2(x0, x1);
+                        put(part * GP + g, c & 0xffu);
+                        if (g + 1 < G)
+                            put(part * GP + g + 1, c >> 8);
+                        if (part < 2) {
+                            // what is left, exactly, times 8
+                            const __half2_raw h =
+                                __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E5M2);
+                            const uint32_t f = (uint32_t)h.x | ((uint32_t)h.y << 16);
+                            x0 = (x0 - ptx::f16lo_to_f32(f)) * 8.f;
+                            x1 = (x1 - ptx::f16hi_to_f32(f)) * 8.f;
+                        }
                     }
                 }
                 if (nv < 32) {
@@ -939,8 +938,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             ptx::tc_fence_after();
             const int segS = R0 + k - j, segE = segS + ns;
             const bool complete = segS >= R0 && segE <= R1;
-            const bool piece_first = segS >= R0;
-            float *ps = p.pieces + (int64_t)(2 * blockIdx.x + (piece_first ? 1 : 0)) * p.slot_floats;
+            float *ps = p.pieces + (int64_t)(2 * blockIdx.x + (segS >= R0 ? 1 : 0)) * p.slot_floats;
             const int nsets = share > 1 ? SETS : 1, e0 = share > 1 ? 0 : set;
             const float *both = stat + (seg & 1) * SETS * 4 * 2 * G;
             // Factors of this warp's accumulators in each set, one head row
@@ -961,7 +959,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                         if (mw != -INFINITY)
                             sum += both[(e * 4 + w) * 2 * G + G + lane] * ptx::ex2(mw - M);
                     }
-                const float inv = !complete ? 1.f : (sum == 0.f ? 0.f : 1.f / (sum * kQ8Weight));
+                const float inv = !complete ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
                 for (int e = e0; e < e0 + nsets; ++e) {
                     const float mw = both[(e * 4 + w4) * 2 * G + lane];
                     fac_s[(e * 4 + w4) * G + lane] = mw == -INFINITY ? 0.f : ptx::ex2(mw - M) * inv;
@@ -981,32 +979,46 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
 #pragma unroll
                     for (int g = 0; g < G; ++g)
                         v[hf][g] = 0.f;
+                // two of the head's accumulators at a time (one, where that
+                // would take 128 registers), all loads in flight
+                constexpr int Y = HALVES * NP <= 32 ? 2 : 1;
+                const int count = nsets << sub_log2;
 #pragma unroll 1
-                for (int x = 0; x < nsets << sub_log2; ++x) {
-                    const int e = e0 + (x >> sub_log2);
-                    const int w = (h << sub_log2) + (x & ((1 << sub_log2) - 1));
-                    const uint32_t at = o_tm + lane_tm + (uint32_t)(e * L::o_cols + w * HALVES * NP);
-                    uint32_t u[HALVES][NP];
+                for (int x = 0; x < count; x += Y) {
+                    uint32_t u[Y][HALVES][NP];
+                    float f[Y][G];
 #pragma unroll
-                    for (int hf = 0; hf < HALVES; ++hf)
+                    for (int y = 0; y < Y; ++y) {
+                        const int xx = x + y < count ? x + y : x;
+                        const int e = e0 + (xx >> sub_log2);
+                        const int w = (h << sub_log2) + (xx & ((1 << sub_log2) - 1));
+                        const uint32_t at =
+                            o_tm + lane_tm + (uint32_t)(e * L::o_cols + w * HALVES * NP);
+                        // (an odd last one is loaded twice and counted once)
 #pragma unroll
-                        for (int c = 0; c < NP / 16; ++c)
-                            ptx::tmem_ld16(at + (uint32_t)(hf * NP + 16 * c),
-                                           *reinterpret_cast<uint32_t(*)[16]>(&u[hf][16 * c]));
-                    float f[G];
+                        for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
-                    for (int g = 0; g < G; ++g)
-                        f[g] = fac_s[(e * 4 + w) * G + g];
-                    ptx::tmem_wait_ld();
-#pragma unroll
-                    for (int hf = 0; hf < HALVES; ++hf) {
-                        ptx::tmem_hold<NP>(u[hf]);
+                            for (int c = 0; c < NP / 16; ++c)
+                                ptx::tmem_ld16(
+                                    at + (uint32_t)(hf * NP + 16 * c),
+                                    *reinterpret_cast<uint32_t(*)[16]>(&u[y][hf][16 * c]));
 #pragma unroll
                         for (int g = 0; g < G; ++g)
-                            v[hf][g] += f[g] * ((__uint_as_float(u[hf][g]) +
-                                                 __uint_as_float(u[hf][GP + g])) +
-                                                __uint_as_float(u[hf][2 * GP + g]));
+                            f[y][g] = x + y < count ? fac_s[(e * 4 + w) * G + g] : 0.f;
                     }
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int y = 0; y < Y; ++y)
+#pragma unroll
+                        for (int hf = 0; hf < HALVES; ++hf) {
+                            ptx::tmem_hold<NP>(u[y][hf]);
+#pragma unroll
+                            for (int g = 0; g < G; ++g)
+                                v[hf][g] += f[y][g] *
+                                            fmaf(fmaf(__uint_as_float(u[y][hf][2 * GP + g]), 0.125f,
+                                                      __uint_as_float(u[y][hf][GP + g])),
+                                                 0.125f, __uint_as_float(u[y][hf][g]));
+                        }
                 }
                 if (complete) {
                     __nv_bfloat16 *o = p.out + ((int64_t)mb * p.num_q_heads + (int64_t)mhg * rows +
@@ -1030,8 +1042,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                     report(p.dev_status, PA_DEV_BAD_BLOCK);
                 if (!complete) {
                     ps[rows * D + 2 * rows] = seg_bad ? 1.f : 0.f;
-                    // the CTA in whose range the segment starts names it
-                    if (piece_first)
+                    if (segS >= R0)
                         *cut_s = make_int4(mb, mhg, cta_of(segE - 1, C, total) - (int)blockIdx.x + 1,
                                            0);
                 }
@@ -1079,71 +1090,76 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
 // part) sums 512 elements of one KV head's accumulators over the pieces of the
 // segment that starts in range x, weighted by 2^(m_i - M) / L, in piece order.
 constexpr int kQ8MaxCtas = 256;
+constexpr int kQ8MergeThreads = 128;
 
-__global__ void __launch_bounds__(128) q8_merge_kernel(const Q8DecodeParams p, int G, int D,
-                                                       int parts)
+// Dynamic shared memory: weights [decode CTAs][G].
+__global__ void __launch_bounds__(kQ8MergeThreads) q8_merge_kernel(const Q8DecodeParams p, int G,
+                                                                   int D, int parts)
 {
-    __shared__ float w[kQ8MaxCtas * 8];
+    extern __shared__ float w[];
     ptx::grid_launch_dependents();
     ptx::grid_wait_prerequisites();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int part = blockIdx.x % parts, rest = blockIdx.x / parts;
     const int h = rest % p.hpc, x = rest / p.hpc;
-    const int4 cut = p.cuts[x];
+    const int4 cut = __ldcg(p.cuts + x);
     const int np = cut.z;
     if (np == 0)
         return;
     const int rows = p.hpc * G;
-    auto piece = [&](int i) {
-        return p.pieces + (int64_t)(i == 0 ? 2 * x + 1 : 2 * (x + i)) * p.slot_floats;
+    const float *base = p.pieces + (int64_t)2 * x * p.slot_floats;
+    auto piece = [&](int i) {                            // slots 2 x + 1, then 2 (x + i)
+        return base + (int64_t)(i == 0 ? 1 : 2 * i) * p.slot_floats;
     };
-    for (int g = warp; g < G; g += 4) {
+    float flag = 0.f;
+    for (int i = tid; i < np; i += kQ8MergeThreads)
+        flag = fmaxf(flag, __ldcg(piece(i) + rows * D + 2 * rows));
+    for (int g = warp; g < G; g += kQ8MergeThreads / 32) {
         const int at = rows * D + 2 * (h * G + g);
-        float M = -INFINITY, Lt = 0.f;
-        for (int i = lane; i < np; i += 32)
-            M = fmaxf(M, piece(i)[at]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+        // (up to 32 pieces: loaded once)
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < np)
+            ml = __ldcg(reinterpret_cast<const float2 *>(piece(lane) + at));
+        float M = ml.x;
+        for (int i = lane + 32; i < np; i += 32)
+            M = fmaxf(M, __ldcg(piece(i) + at));
+        M = ptx::warp_max(M);
+        float sum = 0.f;
         for (int i = lane; i < np; i += 32) {
-            const float m = piece(i)[at];
-            const float f = m == -INFINITY ? 0.f : ptx::ex2(m - M);
-            w[i * 8 + g] = f;
+            if (i >= 32)
+                ml = __ldcg(reinterpret_cast<const float2 *>(piece(i) + at));
+            const float f = ml.x == -INFINITY ? 0.f : ptx::ex2(ml.x - M);
+            w[i * G + g] = f;
             if (f != 0.f)
-                Lt += piece(i)[at + 1] * f;
+                sum += ml.y * f;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
-            Lt += __shfl_xor_sync(kFull, Lt, o);
-        const float inv = Lt > 0.f ? 1.f / (Lt * kQ8Weight) : (Lt == 0.f ? 0.f : Lt);
+            sum += __shfl_xor_sync(kFull, sum, o);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         for (int i = lane; i < np; i += 32)
-            w[i * 8 + g] *= inv;
+            w[i * G + g] *= inv;
     }
-    float flag = 0.f;
-    for (int i = tid; i < np; i += 128)
-        flag = fmaxf(flag, piece(i)[rows * D + 2 * rows]);
     const bool bad = __syncthreads_or(flag != 0.f);      // (also: the weights are in place)
     if (flag == 1.f && h == 0 && part == 0)
         report(p.dev_status, PA_DEV_BAD_BLOCK);
-    const int u = part * 128 + tid;
+    const int u = part * kQ8MergeThreads + tid;          // float4 of the head's accumulators
     if (u >= G * D / 4)
         return;
-    const int g = u / (D / 4), d4 = u - g * (D / 4);
+    const int g = u / (D / 4);
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     if (!bad) {
 #pragma unroll 8
         for (int i = 0; i < np; ++i) {
-            const float4 v =
-                __ldcg(reinterpret_cast<const float4 *>(piece(i) + (h * G + g) * D) + d4);
-            const float f = w[i * 8 + g];
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece(i) + h * G * D) + u);
+            const float f = w[i * G + g];
             sum.x = fmaf(v.x, f, sum.x);
             sum.y = fmaf(v.y, f, sum.y);
             sum.z = fmaf(v.z, f, sum.z);
             sum.w = fmaf(v.w, f, sum.w);
         }
     }
-    store4(p.out + ((int64_t)cut.x * p.num_q_heads + (int64_t)cut.y * rows + h * G + g) * D + 4 * d4,
-           sum);
+    store4(p.out + ((int64_t)cut.x * p.num_q_heads + (int64_t)cut.y * rows + h * G) * D + 4 * u, sum);
 }
 
 }  // namespace pa
