@@ -540,7 +540,7 @@ uint32_t epoch_seed()
     return (uint32_t)x;
 }
 
-uint32_t next_epoch()
+uint32_t new_epoch()
 {
     static std::atomic<uint32_t> counter{epoch_seed()};
     uint32_t e;
@@ -656,6 +656,8 @@ void count_launch() { ++g_launches; }
 unsigned long long test_wait_ns() { return g_test_wait_ns.load(); }
 
 int test_withhold_cta() { return g_test_withhold.load(); }
+
+uint32_t next_epoch() { return new_epoch(); }
 
 // True if the GPU can read and write `ptr` at that same address: device
 // memory, or pinned host memory mapped into the unified address space.
@@ -1102,7 +1104,7 @@ static pa_status decode_entry(void *out, const void *query, const void *k_pool,
         p.counters = reinterpret_cast<unsigned long long *>(
             static_cast<uint8_t *>(workspace) +
             partials_bytes((int64_t)grid * p.geo.hpc, group, head_dim));
-        p.epoch = next_epoch();
+        p.epoch = new_epoch();
     } else {
         p.mode = 1;
     }

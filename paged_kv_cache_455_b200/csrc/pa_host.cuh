@@ -20,6 +20,10 @@ void count_launch();
 unsigned long long test_wait_ns();
 int test_withhold_cta();
 
+// A tag for the arrival counters of one call that splits its work: never 0,
+// distinct for consecutive calls of this process.
+uint32_t next_epoch();
+
 // Tensor map over a pool [nb, bs, Hkv, d] for boxes of `tr` token rows of one
 // head that land in shared memory as [8-row group][128-byte column][row][128
 // bytes], 128-byte swizzled (tr a multiple of 8).  False if it cannot be

@@ -106,6 +106,14 @@ __device__ __forceinline__ float warp_max(float x)
     return y;
 }
 
+// Difference of two pairs of f16.
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // log2, hardware approximation.
 __device__ __forceinline__ float lg2(float x)
 {

@@ -124,20 +124,16 @@ extern "C" pa_status pa_decode_attention_q8(void *out, const void *query, const 
     // too small allows none: then every CTA takes whole segments.
     const int rows = p.hpc * group;
     p.slot_floats = (rows * head_dim + 2 * rows + 1 + 3) / 4 * 4;
-    const size_t cuts_off = (size_t)L.grid * 2 * p.slot_floats * 4;
+    const size_t counters_off = ((size_t)L.grid * 2 * p.slot_floats * 4 + 127) / 128 * 128;
     const bool split = seg_tiles > 1 && L.grid > 1 && workspace != nullptr &&
                        pa::aligned16(workspace) &&
-                       workspace_bytes >= cuts_off + (size_t)L.grid * sizeof(int4);
+                       workspace_bytes >= counters_off + (size_t)L.grid * 128;
     p.mode = split ? 0 : 1;
     if (split) {
         p.pieces = static_cast<float *>(workspace);
-        p.cuts = reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) + cuts_off);
+        p.counters = reinterpret_cast<unsigned long long *>(static_cast<uint8_t *>(workspace) +
+                                                            counters_off);
+        p.epoch = pa::next_epoch();
     }
-    st = run_any(L, head_dim, group, true);
-    if (st != PA_OK || !split)
-        return st;
-    const int parts = std::max(1, group * head_dim / (4 * pa::kQ8MergeThreads));
-    return pa::launch_dependent(pa::q8_merge_kernel, (unsigned)(L.grid * p.hpc * parts),
-                                pa::kQ8MergeThreads, (size_t)(L.grid * group) * 4, stream, p,
-                                group, head_dim, parts);
+    return run_any(L, head_dim, group, true);
 }

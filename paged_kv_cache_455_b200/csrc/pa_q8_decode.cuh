@@ -15,7 +15,9 @@
 //       rows, each as two E4M3 parts; a row uses only its own head's columns
 //       (the tensor cores have room: 128 x NQ x d per 2 * 128 * d bytes)
 //   O^T [128 d x NP] += V_w^T (MN-major, 128 d x 32 tokens) * P_w, for each
-//       warp w and half of d; P_w holds the warp's weights as three E5M2 parts
+//       warp w and half of d; P_w holds the warp's weights as three E5M2 parts,
+//       MN-major too: a token's weights are consecutive, so the lane that has
+//       the token stores them as one or two 16-byte words
 // so no code is ever converted or moved by a thread, and the softmax of one
 // tile is 32 tokens per warp, one per lane.
 //
@@ -43,8 +45,8 @@
 // Work is split as in decode_kernel: every CTA owns an equal, contiguous range
 // of the batch's tiles (mode 0), or whole segments (mode 1); a segment is the
 // run of tiles of one sequence and head group.  The pieces of a segment cut by
-// range borders go to the workspace as fp32 (maximum, sum, accumulator), and
-// q8_merge_kernel joins them after this kernel.
+// range borders go to the workspace as fp32 (maximum, sum, accumulator); the
+// CTA whose piece is the last to arrive joins them after its range.
 #pragma once
 
 #include "pa_kernels.cuh"
@@ -62,8 +64,9 @@ struct Q8DecodeParams {
     const float *k_scales, *v_scales;
     const int32_t *block_tables, *context_lens;
     float *pieces;           // mode 0: two slots per CTA
-    int4 *cuts;              // mode 0, per CTA: sequence, head group and pieces of the
-                             // segment that starts in its range and runs past it (0: none)
+    unsigned long long *counters;   // mode 0: arrivals at the cut segment that starts in a
+                                    // CTA's range, a line each (see segment_arrive)
+    uint32_t epoch;          // mode 0: tag of this call's counts (never 0)
     int32_t *dev_status;
     int64_t num_blocks;
     int num_seqs, num_q_heads, num_kv_heads;
@@ -104,7 +107,7 @@ struct Q8Smem {
     static constexpr int kSets = 128 + 2 * o_cols <= 512 ? 2 : 1;
     static constexpr uint32_t tmem_cols = 128 + kSets * o_cols <= 256 ? 256u : 512u;
     static constexpr int kSoftmax = 4 * kSets;                       // warps
-    static constexpr int kThreads = 32 * (kSoftmax + 6);
+    static constexpr int kThreads = 32 * (kSoftmax + 8);
     static constexpr int v_off = kStages * kStage;
     static constexpr int q_off = kQ8SmemStages;
     static constexpr int p_off = q_off + kQBufs * kQRows * D;
@@ -114,8 +117,10 @@ struct Q8Smem {
     static constexpr int stat_off = sf_off + 4 * 4 * G * 4;          // [2][sets][4][m, l][G]
     static constexpr int fac_off = stat_off + 2 * kSets * 4 * 2 * G * 4;   // [sets][4][G]
     static constexpr int alpha_off = fac_off + kSets * 4 * G * 4;    // [sets][4][G]
-    static constexpr int cut_off = (alpha_off + kSets * 4 * G * 4 + 15) / 16 * 16;
-    static constexpr int bar_off = cut_off + 16;
+    static constexpr int pend_off = (alpha_off + kSets * 4 * G * 4 + 15) / 16 * 16;
+    static constexpr int bar_off = pend_off + 32;
+    // a merge's weights lie where the queries and the weights of P were
+    static_assert(meta_off - q_off >= 148 * 4 * G * 4, "room for a merge's weights");
     static constexpr int kBars = 5 * kStages + 8 + 2 * kQBufs + 5;
     static constexpr int flag_off = bar_off + 8 * kBars;   // abort, tensor memory, tiles done
     static constexpr int cbase_off = flag_off + 16;
@@ -241,9 +246,13 @@ __device__ __forceinline__ uint32_t e5m2x2(float lo, float hi)
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
 }
 
-__device__ __forceinline__ void st_shared_u8(uint32_t a, uint32_t v)
+// Two f16 values to E4M3 codes.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t x)
 {
-    asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+    __half2_raw h;
+    h.x = (unsigned short)(x & 0xffffu);
+    h.y = (unsigned short)(x >> 16);
+    return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
 }
 
 template <int D, int G>
@@ -267,10 +276,11 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
     float *stat = reinterpret_cast<float *>(gen + L::stat_off);
     float *fac_s = reinterpret_cast<float *>(gen + L::fac_off);
     float *alpha_s = reinterpret_cast<float *>(gen + L::alpha_off);
-    int4 *cut_s = reinterpret_cast<int4 *>(gen + L::cut_off);
+    // merges this CTA owes: first CTA, pieces, sequence, head group
+    int4 *pend_s = reinterpret_cast<int4 *>(gen + L::pend_off);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + L::flag_off);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen + L::flag_off + 4);
-    volatile int *tiles_done = reinterpret_cast<volatile int *>(gen + L::flag_off + 8);
+    int *tiles_done = reinterpret_cast<int *>(gen + L::flag_off + 8);
     int *cbase = reinterpret_cast<int *>(gen + L::cbase_off);
     const uint32_t bars = base + L::bar_off;
     const uint32_t kfull = bars, kempty = kfull + 8 * S, vfull = kempty + 8 * S,
@@ -291,7 +301,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             ptx::mbar_init(pvdone + 8 * i, 1);
         }
         for (int i = 0; i < QB; ++i) {
-            ptx::mbar_init(qfull + 8 * i, 2);
+            ptx::mbar_init(qfull + 8 * i, 4);
             ptx::mbar_init(qempty + 8 * i, 1);
         }
         ptx::mbar_init(ofree, 4);
@@ -301,13 +311,9 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
         ptx::mbar_init(drain_o, 1);
         *abort_flag = 0;
         *tiles_done = 0;
-        *cut_s = make_int4(0, 0, 0, 0);
+        pend_s[0] = pend_s[1] = make_int4(0, 0, 0, 0);
     }
     ptx::fence_mbar_init();
-    // weight rows that no head fills stay zero
-    for (int i = tid; i < 2 * 4 * L::kP / 16; i += L::kThreads)
-        reinterpret_cast<uint4 *>(gen + L::p_off)[i] = make_uint4(0, 0, 0, 0);
-    ptx::fence_proxy_async_smem();
     if (warp == W_S) {
         ptx::tmem_alloc(ptx::smem_u32(tmem_holder), L::tmem_cols);
         ptx::tmem_relinquish();
@@ -333,6 +339,13 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
         if (__any_sync(kFull, *abort_flag != 0))
             return false;
         return __all_sync(kFull, ptx::mbar_wait_bounded(bar, parity, lim));
+    };
+    // One thread: counts this CTA's piece of the cut segment [segS, segE) in;
+    // whoever completes the count owes the merge.
+    auto arrive_piece = [&](int segS, int segE, int b, int hg) {
+        const int x0 = cta_of(segS, C, total), np = cta_of(segE - 1, C, total) - x0 + 1;
+        if (segment_arrive(p.counters + (int64_t)x0 * kLineWords, p.epoch) == np)
+            pend_s[segS >= R0 ? 0 : 1] = make_int4(x0, np, b, hg);
     };
     auto give_up = [&]() {
         if (lane == 0) {
@@ -529,7 +542,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
         __syncwarp();
     } else if (warp == W_O) {
         // ============================================================ O^T
-        constexpr uint32_t idesc = ptx::umma_idesc_f8(128, NP, false, true, true, false);
+        constexpr uint32_t idesc = ptx::umma_idesc_f8(128, NP, false, true, true, true);
         bool ok = true;
         for (int k = 0; k < nk; ++k) {
             const int s = k % S;
@@ -551,7 +564,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             if (ptx::elect_one()) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    const uint64_t bd = ptx::umma_desc_plain(pst + w * L::kP, 128, 256);
+                    const uint64_t bd = ptx::umma_desc_plain(pst + w * L::kP, 128, 512);
 #pragma unroll
                     for (int h = 0; h < HALVES; ++h)
                         ptx::umma_f8_ss(acc + (uint32_t)((w * HALVES + h) * NP),
@@ -590,15 +603,15 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                 const int rows = hpc * G;
                 const __nv_bfloat16 *src = p.q + ((int64_t)w.b * p.num_q_heads +
                                                   (int64_t)w.hg * rows) * D;
-                constexpr int RW = 4 * G / 2;            // rows per warp, at most
-                constexpr int RB = RW < 8 ? RW : 8;      // rows loaded at once
+                constexpr int RW = G;                    // rows per warp, at most
+                constexpr int RB = RW < 4 ? RW : 4;      // rows loaded at once
                 bool free = seg < QB;
 #pragma unroll 1
                 for (int r0 = 0; r0 < RW; r0 += RB) {
                     uint32_t x[RB][E / 2];
 #pragma unroll
                     for (int i = 0; i < RB; ++i) {
-                        const int r = 2 * (r0 + i) + (warp - W_Q);
+                        const int r = 4 * (r0 + i) + (warp - W_Q);
 #pragma unroll
                         for (int e = 0; e < E / 2; ++e)
                             x[i][e] = 0;
@@ -630,7 +643,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                     const uint32_t qst = base + (uint32_t)(L::q_off + qb * L::kQRows * D);
 #pragma unroll
                     for (int i = 0; i < RB; ++i) {
-                        const int r = 2 * (r0 + i) + (warp - W_Q);
+                        const int r = 4 * (r0 + i) + (warp - W_Q);
                         if (r >= rows)
                             continue;
                         uint32_t top = 0;
@@ -646,12 +659,14 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                             uint32_t h2[2], l2[2];
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const float y0 = ptx::bf16lo_to_f32(x[i][2 * e + k]) * sigma;
-                                const float y1 = ptx::bf16hi_to_f32(x[i][2 * e + k]) * sigma;
-                                h2[k] = f32x2_to_e4m3x2(y0, y1);
-                                const uint32_t f = e4m3x2_to_f16x2(h2[k]);
-                                l2[k] = f32x2_to_e4m3x2(y0 - ptx::f16lo_to_f32(f),
-                                                        y1 - ptx::f16hi_to_f32(f));
+                                // (8 bits of a value below 256: exact in f16 but
+                                // far below E4M3's quantum, and so is what is left)
+                                const uint32_t y =
+                                    ptx::pack_f16x2(ptx::bf16lo_to_f32(x[i][2 * e + k]) * sigma,
+                                                    ptx::bf16hi_to_f32(x[i][2 * e + k]) * sigma);
+                                h2[k] = f16x2_to_e4m3x2(y);
+                                l2[k] = f16x2_to_e4m3x2(
+                                    ptx::sub_f16x2(y, e4m3x2_to_f16x2(h2[k])));
                             }
                             hi[e] = h2[0] | (h2[1] << 16);
                             lo[e] = l2[0] | (l2[1] << 16);
@@ -705,6 +720,11 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
         const int rows = hpc * G;
         // outputs and the workspace may be in use by the kernel ahead
         ptx::grid_wait_prerequisites();
+        // this CTA's counter starts the call at (epoch, 0), unless an arrival
+        // has already counted in it
+        if (p.mode == 0 && tid == 0)
+            ptx::red_max_relaxed_gpu_u64(p.counters + (int64_t)blockIdx.x * kLineWords,
+                                         (unsigned long long)p.epoch << 32);
         for (int b = blockIdx.x; set == 0 && b < p.num_seqs; b += gridDim.x) {
             const int len = p.context_lens[b];
             if (eff_ctx(len, p.ctx_cap) > 0)
@@ -738,7 +758,8 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             wait(mfull + 8 * s, (uint32_t)((k / S) & 1));
             bool first = false, over = false;
             int n = 0, j = 0, seg = 0;
-            float t[G], lv = 0.f, vs = 0.f;
+            float t[G], room = 0.f, lv = 0.f, vs = 0.f;
+            bool seen = false;
             if (!fail) {
                 n = meta[s].n;
                 j = meta[s].j;
@@ -760,28 +781,28 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                 uint32_t u[2 * G];
                 ptx::tmem_ld<2 * G>(tmem + (uint32_t)((k & 1) * 64 + hl * 2 * G) + lane_tm, u);
                 lv = fmaxf(ptx::lg2(vs), -64.f);
+                room = kQ8Grow - lv;
+                seen = tok < n;
                 ptx::tmem_wait_ld();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (!fail && lane == 0)
+                if (lane == 0)
                     ptx::mbar_arrive(sfree + 8 * (k & 1));
                 ptx::tmem_hold<2 * G>(u);
-                const bool seen = tok < n;
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const float sg = (__uint_as_float(u[g]) + __uint_as_float(u[G + g])) *
-                                     (fac[g] * ks);
-                    t[g] = seen ? sg : -INFINITY;
-                }
+                for (int g = 0; g < G; ++g)
+                    t[g] = (__uint_as_float(u[g]) + __uint_as_float(u[G + g])) * (fac[g] * ks);
                 if (first) {
 #pragma unroll
                     for (int g = 0; g < G; ++g)
-                        m[g] = ptx::warp_max(t[g] + lv);
+                        m[g] = ptx::warp_max(seen ? t[g] + lv : -INFINITY);
                 }
                 // (a warp without tokens so far has m = -inf: any token is over)
+                float top = t[0] - m[0];
 #pragma unroll
-                for (int g = 0; g < G; ++g)
-                    over |= t[g] + lv > m[g] + kQ8Grow;
+                for (int g = 1; g < G; ++g)
+                    top = fmaxf(top, t[g] - m[g]);
+                over = seen && top > room;
             }
             if (ptx::barrier_or(bar0, 128, over || fail)) {
                 if (ptx::barrier_or(bar0 + 1, 128, fail))
@@ -790,7 +811,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                 bool scale_o = false;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float mx = ptx::warp_max(t[g] + lv);
+                    const float mx = ptx::warp_max(seen ? t[g] + lv : -INFINITY);
                     float al = 1.f;
                     if (mx > m[g] + kQ8Grow) {
                         // (from -inf there is nothing to rescale)
@@ -846,35 +867,47 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                 wait(vfull + 8 * s, (uint32_t)((k / S) & 1));
             if (!fail) {
                 const uint32_t pw = base + (uint32_t)(L::p_off + ((k & 1) * 4 + w4) * L::kP +
-                                                      (lane >> 4) * 128 + (lane & 15));
-                auto put = [&](int row, uint32_t v) {
-                    st_shared_u8(pw + (uint32_t)((row >> 3) * 256 + (row & 7) * 16), v);
-                };
-                float x[G];
+                                                      (lane >> 3) * 128 + (lane & 7) * 16);
+                float x[2 * ((G + 1) / 2)];
+                const float vsx = seen ? vs : 0.f;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float e = lane < nv ? ptx::ex2(t[g] - m[g]) : 0.f;
+                    const float e = ptx::ex2(seen ? t[g] - m[g] : -INFINITY);
                     l[g] += e;
-                    x[g] = lane < nv ? e * vs : 0.f;
+                    x[g] = e * vsx;
                 }
+                if constexpr (G % 2)
+                    x[G] = 0.f;
+                uint32_t word[3][GP / 4];                 // part, four heads
+#pragma unroll
+                for (int q = 0; q < GP / 4; ++q)
+                    word[0][q] = word[1][q] = word[2][q] = 0;
 #pragma unroll
                 for (int g = 0; g < G; g += 2) {
-                    float x0 = x[g], x1 = g + 1 < G ? x[g + 1 < G ? g + 1 : g] : 0.f;
+                    float x0 = x[g], x1 = x[g + 1];
 #pragma unroll
                     for (int part = 0; part < 3; ++part) {
                         const uint32_t c = e5m2x2(x0, x1);
-                        put(part * GP + g, c & 0xffu);
-                        if (g + 1 < G)
-                            put(part * GP + g + 1, c >> 8);
+                        word[part][g / 4] |= c << (8 * (g & 3));
                         if (part < 2) {
-                            // what is left, exactly, times 8
-                            const __half2_raw h =
-                                __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E5M2);
-                            const uint32_t f = (uint32_t)h.x | ((uint32_t)h.y << 16);
+                            // what is left, exactly, times 8 (a code is the
+                            // upper byte of its f16)
+                            const uint32_t f = ptx::prmt(c, 0, 0x1404);
                             x0 = (x0 - ptx::f16lo_to_f32(f)) * 8.f;
                             x1 = (x1 - ptx::f16hi_to_f32(f)) * 8.f;
                         }
                     }
+                }
+                auto put = [&](uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a),
+                                 "r"(b), "r"(c), "r"(d)
+                                 : "memory");
+                };
+                if constexpr (GP == 4) {
+                    put(pw, word[0][0], word[1][0], word[2][0], 0);
+                } else {
+                    put(pw, word[0][0], word[0][GP / 4 - 1], word[1][0], word[1][GP / 4 - 1]);
+                    put(pw + 512, word[2][0], word[2][GP / 4 - 1], 0, 0);
                 }
                 if (nv < 32) {
                     // V rows past the sequence hold whatever was there; their
@@ -941,38 +974,56 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             float *ps = p.pieces + (int64_t)(2 * blockIdx.x + (segS >= R0 ? 1 : 0)) * p.slot_floats;
             const int nsets = share > 1 ? SETS : 1, e0 = share > 1 ? 0 : set;
             const float *both = stat + (seg & 1) * SETS * 4 * 2 * G;
-            // Factors of this warp's accumulators in each set, one head row
-            // per lane: 2^(m - M) over the row's sets and warps, over the sum
-            // when the segment is complete.
-            for (int e = e0; e < e0 + nsets; ++e)
-                for (int w = 0; w < 4; ++w)
-                    seg_bad |= both[(e * 4 + w) * 2 * G + G] == -1.f;
-            if (lane < G) {
-                const int w0 = hl << sub_log2;
-                float M = -INFINITY, sum = 0.f;
-                for (int e = e0; e < e0 + nsets; ++e)
-                    for (int w = w0; w < w0 + (1 << sub_log2); ++w)
-                        M = fmaxf(M, both[(e * 4 + w) * 2 * G + lane]);
-                for (int e = e0; e < e0 + nsets; ++e)
-                    for (int w = w0; w < w0 + (1 << sub_log2); ++w) {
-                        const float mw = both[(e * 4 + w) * 2 * G + lane];
-                        if (mw != -INFINITY)
-                            sum += both[(e * 4 + w) * 2 * G + G + lane] * ptx::ex2(mw - M);
-                    }
-                const float inv = !complete ? 1.f : (sum == 0.f ? 0.f : 1.f / sum);
-                for (int e = e0; e < e0 + nsets; ++e) {
-                    const float mw = both[(e * 4 + w4) * 2 * G + lane];
-                    fac_s[(e * 4 + w4) * G + lane] = mw == -INFINITY ? 0.f : ptx::ex2(mw - M) * inv;
+            // Factors of this warp's accumulators in each set: 2^(m - M) over
+            // the head row's sets and warps, over the sum when the segment is
+            // complete.  Lane (and lane + 32) holds item x * G + g: head row g
+            // in the x-th of the head's nx accumulators.
+            const int nx = nsets << sub_log2, w0 = hl << sub_log2;
+            float mi[2], li[2], fi[2], M = -INFINITY, sum = 0.f;
+            bool marked = false;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int x = (lane + 32 * q) / G, g = lane % G;
+                const int e = e0 + (x >> sub_log2), w = w0 + (x & ((1 << sub_log2) - 1));
+                mi[q] = -INFINITY;
+                li[q] = 0.f;
+                if (x < nx) {
+                    mi[q] = both[(e * 4 + w) * 2 * G + g];
+                    li[q] = both[(e * 4 + w) * 2 * G + G + g];
                 }
-                if (!complete && (w4 & ((1 << sub_log2) - 1)) == 0) {
-                    ps[rows * D + 2 * (hl * G + lane)] = M;
-                    ps[rows * D + 2 * (hl * G + lane) + 1] = sum;
-                }
+                marked |= li[q] == -1.f;
+                M = fmaxf(M, mi[q]);
             }
+            seg_bad |= __any_sync(kFull, marked);
+#pragma unroll
+            for (int o = G; o < 32; o <<= 1)
+                M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                fi[q] = mi[q] == -INFINITY ? 0.f : ptx::ex2(mi[q] - M);
+                sum += mi[q] == -INFINITY ? 0.f : li[q] * fi[q];
+            }
+#pragma unroll
+            for (int o = G; o < 32; o <<= 1)
+                sum += __shfl_xor_sync(kFull, sum, o);
+            const float inv = !complete ? 1.f : (sum == 0.f ? 0.f : __frcp_rn(sum));
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int x = (lane + 32 * q) / G;
+                const int e = e0 + (x >> sub_log2), w = w0 + (x & ((1 << sub_log2) - 1));
+                if (x < nx && w == w4)
+                    fac_s[(e * 4 + w) * G + lane % G] = fi[q] * inv;
+            }
+            if (!complete && w0 == w4 && lane < G)
+                *reinterpret_cast<float2 *>(ps + rows * D + 2 * (hl * G + lane)) =
+                    make_float2(M, sum);
             if (ptx::barrier_or(bar0, 128, false))
                 break;                                        // (never: orders the factors)
+            __nv_bfloat16 *oc = p.out + ((int64_t)mb * p.num_q_heads + (int64_t)mhg * rows) * D +
+                                w4 * 32 + lane;
+            float *op = ps + w4 * 32 + lane;
 #pragma unroll 1
-            for (int h = 0; h < hpc; ++h) {
+            for (int h = 0; h < hpc; ++h, oc += G * D, op += G * D) {
                 float v[HALVES][G];
 #pragma unroll
                 for (int hf = 0; hf < HALVES; ++hf)
@@ -1021,38 +1072,38 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                         }
                 }
                 if (complete) {
-                    __nv_bfloat16 *o = p.out + ((int64_t)mb * p.num_q_heads + (int64_t)mhg * rows +
-                                                h * G) * D + w4 * 32 + lane;
 #pragma unroll
                     for (int g = 0; g < G; ++g)
 #pragma unroll
                         for (int hf = 0; hf < HALVES; ++hf)
-                            o[g * D + hf * 128] = __float2bfloat16_rn(seg_bad ? 0.f : v[hf][g]);
+                            oc[g * D + hf * 128] = __float2bfloat16_rn(seg_bad ? 0.f : v[hf][g]);
                 } else {
-                    float *o = ps + h * G * D + w4 * 32 + lane;
 #pragma unroll
                     for (int g = 0; g < G; ++g)
 #pragma unroll
                         for (int hf = 0; hf < HALVES; ++hf)
-                            o[g * D + hf * 128] = v[hf][g];
+                            op[g * D + hf * 128] = v[hf][g];
                 }
-            }
-            if (st == 0) {
-                if (complete && seg_bad)
-                    report(p.dev_status, PA_DEV_BAD_BLOCK);
-                if (!complete) {
-                    ps[rows * D + 2 * rows] = seg_bad ? 1.f : 0.f;
-                    if (segS >= R0)
-                        *cut_s = make_int4(mb, mhg, cta_of(segE - 1, C, total) - (int)blockIdx.x + 1,
-                                           0);
-                }
-                *tiles_done = k + 1;
             }
             // O may be overwritten
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0)
                 ptx::mbar_arrive(ofree);
+            if (!complete) {
+                if (st == 0)
+                    ps[rows * D + 2 * rows] = seg_bad ? 1.f : 0.f;
+                // the set's stores, then the arrival that releases them
+                if (ptx::barrier_or(bar0, 128, false))
+                    break;                                    // (never)
+                if (st == 0)
+                    arrive_piece(segS, segE, mb, mhg);
+            } else if (seg_bad && st == 0) {
+                report(p.dev_status, PA_DEV_BAD_BLOCK);
+            }
+            // (the other set may be past its next segment already)
+            if (st == 0)
+                atomicMax(tiles_done, k + 1);
         }
     }
     ptx::tc_fence_before();
@@ -1074,92 +1125,99 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             } else if (tid == 0) {
                 float *ps = p.pieces + (int64_t)(2 * blockIdx.x + (w.g0 >= R0 ? 1 : 0)) * p.slot_floats;
                 ps[rows * D + 2 * rows] = 2.f;
-                if (w.g0 >= R0)
-                    *cut_s = make_int4(w.b, w.hg, cta_of(segE - 1, C, total) - (int)blockIdx.x + 1, 0);
+                arrive_piece(w.g0, segE, w.b, w.hg);
             }
             if (segE >= R1)
                 break;
             q8_walk_next(w, p, lane);
         }
+        __syncthreads();
     }
-    if (p.mode == 0 && tid == 0)
-        p.cuts[blockIdx.x] = *cut_s;
-}
-
-// Joins the pieces of every segment that range borders cut: CTA (x, head,
-// part) sums 512 elements of one KV head's accumulators over the pieces of the
-// segment that starts in range x, weighted by 2^(m_i - M) / L, in piece order.
-constexpr int kQ8MaxCtas = 256;
-constexpr int kQ8MergeThreads = 128;
-
-// Dynamic shared memory: weights [decode CTAs][G].
-__global__ void __launch_bounds__(kQ8MergeThreads) q8_merge_kernel(const Q8DecodeParams p, int G,
-                                                                   int D, int parts)
-{
-    extern __shared__ float w[];
-    ptx::grid_launch_dependents();
-    ptx::grid_wait_prerequisites();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int part = blockIdx.x % parts, rest = blockIdx.x / parts;
-    const int h = rest % p.hpc, x = rest / p.hpc;
-    const int4 cut = __ldcg(p.cuts + x);
-    const int np = cut.z;
-    if (np == 0)
-        return;
-    const int rows = p.hpc * G;
-    const float *base = p.pieces + (int64_t)2 * x * p.slot_floats;
-    auto piece = [&](int i) {                            // slots 2 x + 1, then 2 (x + i)
-        return base + (int64_t)(i == 0 ? 1 : 2 * i) * p.slot_floats;
-    };
-    float flag = 0.f;
-    for (int i = tid; i < np; i += kQ8MergeThreads)
-        flag = fmaxf(flag, __ldcg(piece(i) + rows * D + 2 * rows));
-    for (int g = warp; g < G; g += kQ8MergeThreads / 32) {
-        const int at = rows * D + 2 * (h * G + g);
-        // (up to 32 pieces: loaded once)
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane < np)
-            ml = __ldcg(reinterpret_cast<const float2 *>(piece(lane) + at));
-        float M = ml.x;
-        for (int i = lane + 32; i < np; i += 32)
-            M = fmaxf(M, __ldcg(piece(i) + at));
-        M = ptx::warp_max(M);
-        float sum = 0.f;
-        for (int i = lane; i < np; i += 32) {
-            if (i >= 32)
-                ml = __ldcg(reinterpret_cast<const float2 *>(piece(i) + at));
-            const float f = ml.x == -INFINITY ? 0.f : ptx::ex2(ml.x - M);
-            w[i * G + g] = f;
-            if (f != 0.f)
-                sum += ml.y * f;
-        }
+    // ---- the merges this CTA owes, all its threads:
+    //   M = max_i m_i,  L = sum_i l_i 2^(m_i - M),  o = sum_i a_i 2^(m_i - M) / L
+    // over the pieces i, in piece order, so that the result does not depend on
+    // which arrival was the last.
+    float *wt = reinterpret_cast<float *>(gen + L::q_off);        // [pieces][rows]
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const int4 pend = pend_s[i];
+        const int x0 = pend.x, np = pend.y;
+        if (np == 0)
+            continue;
+        const int rows = hpc * G;
+        const float *first = p.pieces + (int64_t)2 * x0 * p.slot_floats;
+        auto piece = [&](int c) {                        // slots 2 x0 + 1, then 2 (x0 + c)
+            return first + (int64_t)(c == 0 ? 1 : 2 * c) * p.slot_floats;
+        };
+        float flag = 0.f;
+        for (int c = tid; c < np; c += L::kThreads)
+            flag = fmaxf(flag, __ldcg(piece(c) + rows * D + 2 * rows));
+#pragma unroll 1
+        for (int r = warp; r < rows; r += L::kThreads / 32) {
+            const int at = rows * D + 2 * r;
+            // (up to 32 pieces: loaded once)
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (lane < np)
+                ml = __ldcg(reinterpret_cast<const float2 *>(piece(lane) + at));
+            float M = ml.x, sum = 0.f;
+            for (int c = lane + 32; c < np; c += 32)
+                M = fmaxf(M, __ldcg(piece(c) + at));
+            M = ptx::warp_max(M);
+            for (int c = lane; c < np; c += 32) {
+                if (c >= 32)
+                    ml = __ldcg(reinterpret_cast<const float2 *>(piece(c) + at));
+                const float f = ml.x == -INFINITY ? 0.f : ptx::ex2(ml.x - M);
+                wt[c * rows + r] = f;
+                if (f != 0.f)
+                    sum += ml.y * f;
+            }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            sum += __shfl_xor_sync(kFull, sum, o);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        for (int i = lane; i < np; i += 32)
-            w[i * G + g] *= inv;
-    }
-    const bool bad = __syncthreads_or(flag != 0.f);      // (also: the weights are in place)
-    if (flag == 1.f && h == 0 && part == 0)
-        report(p.dev_status, PA_DEV_BAD_BLOCK);
-    const int u = part * kQ8MergeThreads + tid;          // float4 of the head's accumulators
-    if (u >= G * D / 4)
-        return;
-    const int g = u / (D / 4);
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!bad) {
-#pragma unroll 8
-        for (int i = 0; i < np; ++i) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(piece(i) + h * G * D) + u);
-            const float f = w[i * G + g];
-            sum.x = fmaf(v.x, f, sum.x);
-            sum.y = fmaf(v.y, f, sum.y);
-            sum.z = fmaf(v.z, f, sum.z);
-            sum.w = fmaf(v.w, f, sum.w);
+            for (int o = 16; o > 0; o >>= 1)
+                sum += __shfl_xor_sync(kFull, sum, o);
+            const float inv = sum == 0.f ? 0.f : __frcp_rn(sum);
+            for (int c = lane; c < np; c += 32)
+                wt[c * rows + r] *= inv;
         }
+        const bool bad = __syncthreads_or(flag != 0.f);  // (also: the weights are in place)
+        if (flag == 1.f)
+            report(p.dev_status, PA_DEV_BAD_BLOCK);
+        __nv_bfloat16 *o = p.out + ((int64_t)pend.z * p.num_q_heads + (int64_t)pend.w * rows) * D;
+        // two float4s per thread at a time, eight pieces of each in flight
+        const int units = rows * D / 4;
+#pragma unroll 1
+        for (int u = tid; u < units; u += 2 * L::kThreads) {
+            const int u2 = u + L::kThreads < units ? u + L::kThreads : u;
+            const int ra = u / (D / 4), rb = u2 / (D / 4);
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+            const float *src = piece(0);
+            if (!bad) {
+#pragma unroll 8
+                for (int c = 0; c < np; ++c) {
+                    const float4 va = __ldcg(reinterpret_cast<const float4 *>(src) + u);
+                    const float4 vb = __ldcg(reinterpret_cast<const float4 *>(src) + u2);
+                    src = first + (int64_t)2 * (c + 1) * p.slot_floats;
+                    const float fa = wt[c * rows + ra], fb = wt[c * rows + rb];
+                    a.x = fmaf(va.x, fa, a.x);
+                    a.y = fmaf(va.y, fa, a.y);
+                    a.z = fmaf(va.z, fa, a.z);
+                    a.w = fmaf(va.w, fa, a.w);
+                    b.x = fmaf(vb.x, fb, b.x);
+                    b.y = fmaf(vb.y, fb, b.y);
+                    b.z = fmaf(vb.z, fb, b.z);
+                    b.w = fmaf(vb.w, fb, b.w);
+                }
+            }
+            store4(o + 4 * u, a);
+            if (u2 != u)
+                store4(o + 4 * u2, b);
+        }
+        // the count starts again from nothing, whatever tag the next call has
+        if (tid == 0)
+            ptx::st_relaxed_gpu_u64(p.counters + (int64_t)x0 * kLineWords, 0);
+        __syncthreads();
     }
-    store4(p.out + ((int64_t)cut.x * p.num_q_heads + (int64_t)cut.y * rows + h * G) * D + 4 * u, sum);
 }
+
+constexpr int kQ8MaxCtas = 148;   // (a merge's weights have room for so many pieces)
 
 }  // namespace pa

@@ -254,3 +254,56 @@ def test_prefill_bad_blocks_and_lengths(pa):
     cu = c.cu
     assert (out[cu[1]:cu[3]] == 0).all()
     assert torch.equal(out[:cu[1]], want[:cu[1]]) and torch.equal(out[cu[3]:], want[cu[3]:])
+
+
+def test_decode_captured_once_and_replayed(pa):
+    # one call per graph, two graphs that share the workspace, replayed in turn
+    cases = [Case(22, [3000, 20, 1700, 900], 16, 4, 256, 16), Case(23, [5000, 640], 8, 1, 128, 32)]
+    want = [c.decode(pa) for c in cases]
+    ws = torch.full((max(pa.pa_decode_workspace_bytes(4, 16, 4, 256, 3000),
+                         pa.pa_decode_workspace_bytes(2, 8, 1, 128, 5000)),), 255,
+                    dtype=torch.uint8, device=DEV)
+    side, graphs, outs, keep = torch.cuda.Stream(DEV), [], [], []
+    for c in cases:
+        args = (*c.device(), _dev(c.tab), _dev(c.lens))
+        out = torch.zeros_like(c.q)
+        keep.append(args)
+        outs.append(out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+            pa.pa_decode_attention_q8(out, c.q, *args, int(c.lens.max()), c.scale, ws)
+        graphs.append(g)
+    for which in (0, 0, 1, 0, 1, 1):
+        outs[which].fill_(float("nan"))
+        graphs[which].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[which], want[which])
+    del graphs
+
+
+@pytest.mark.parametrize("cta", [0, 70, 147])
+def test_decode_wait_that_runs_out(pa, cta):
+    # CTA `cta` never gets its second tile: its waits end after the limit, the
+    # sequences it held from there on are zeros, the rest is right, and the
+    # workspace serves the next call
+    c = Case(24, [3000] * 12, 16, 4, 256, 16)
+    want = c.decode(pa)
+    ws = torch.zeros(pa.pa_decode_workspace_bytes(12, 16, 4, 256, 3000), dtype=torch.uint8,
+                     device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pa.testing_set_wait_limit_ns(20_000_000)
+    pa.testing_withhold_copy(cta)
+    try:
+        out = c.decode(pa, status=status, ws=ws)
+    finally:
+        pa.testing_withhold_copy(-1)
+        pa.testing_set_wait_limit_ns(0)
+    assert int(status.item()) == pa.PA_DEV_WAIT_TIMEOUT
+    tiles = -(-3000 // 32)
+    total = 12 * tiles
+    r0, r1 = cta * total // 148, (cta + 1) * total // 148
+    lost = {t // tiles for t in range(r0, r1)}
+    for b in range(12):
+        assert (out[b] == 0).all() if b in lost else torch.equal(out[b], want[b])
+    assert torch.equal(c.decode(pa, ws=ws), want)
