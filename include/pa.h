@@ -467,9 +467,9 @@ pa_status pa_rope_and_cache(void *query_out, int64_t query_out_stride, const voi
  * outside [0, max_position) sets PA_DEV_BAD_POSITION: that token is not cached
  * and its query_out row is zeros.  Two sequences must not append to the same
  * block in one call.
- * The kernel lets the next one on the stream start early; it writes none of
- * the arrays that pa_decode_attention reads before it waits, so long as the
- * pools are not also given to that call or to pa_decode_attention_fp8.
+ * With max_q_len 1 the kernel lets the next one on the stream start early
+ * (see pa_decode_attention_q8; the pools are not to be given to
+ * pa_decode_attention_fp8 as well).
  */
 pa_status pa_rope_and_cache_q8(void *query_out, int64_t query_out_stride, const void *query,
                                int64_t query_stride, const void *key, int64_t key_stride,
@@ -491,12 +491,16 @@ pa_status pa_rope_and_cache_q8(void *query_out, int64_t query_out_stride, const 
  * without it each sequence is processed by one CTA per group of KV heads).
  * Arithmetic: both tile products on E4M3 tensor cores with the codes as stored
  * and fp32 accumulation; query rows and softmax weights are each carried as
- * two E4M3 parts, as in pa_decode_attention_fp8.  A weight includes its
- * block's V scale before it is split, and the running reference of the
- * weights is the largest weight so scaled (rescaled once it grows by 2^4), so
- * that its error is relative to what contributes most to the output; the row
- * sums use the fp32 weights.  Nothing is read of pools, scales or query before
- * the kernel ahead on the stream has completed.
+ * two E4M3 parts, as in pa_decode_attention_fp8 (three E5M2 parts for the
+ * weights).  A weight includes its block's V scale before it is split, and the
+ * weights are kept relative to the largest so scaled, so that their errors are
+ * relative to what contributes most to the output; the row
+ * sums use the fp32 weights.
+ * Before the kernel ahead on the stream has completed, the kernel reads
+ * context_lens, block_tables, and the pool rows and scales of blocks other
+ * than each sequence's last one: a kernel ahead that allows an early start
+ * must not write those.  pa_rope_and_cache_q8 allows one only when max_q_len
+ * is 1, and then writes in last blocks alone.
  */
 pa_status pa_decode_attention_q8(void *out, const void *query, const void *k_pool,
                                  const void *v_pool, const float *k_scales, const float *v_scales,

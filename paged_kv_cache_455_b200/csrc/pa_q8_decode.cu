@@ -134,6 +134,17 @@ extern "C" pa_status pa_decode_attention_q8(void *out, const void *query, const 
         p.counters = reinterpret_cast<unsigned long long *>(static_cast<uint8_t *>(workspace) +
                                                             counters_off);
         p.epoch = pa::next_epoch();
+        // Pieces of a segment, when all are as long as the longest: from six on
+        // a kernel of its own joins them (eight 8K contexts, 19 pieces: MEASURE
+        // us with it, MEASURE us without; 64 contexts of up to 4K, 3 pieces:
+        // MEASURE us with it, MEASURE us without).
+        const int64_t segments = num_seqs * (int64_t)p.head_groups;
+        p.merge_later = num_seqs <= 32 && L.grid >= 6 * segments;
     }
-    return run_any(L, head_dim, group, true);
+    st = run_any(L, head_dim, group, true);
+    if (st != PA_OK || !p.merge_later)
+        return st;
+    return pa::launch_dependent(pa::q8_merge_kernel,
+                                (unsigned)(num_seqs * p.head_groups * p.hpc * group * head_dim / 128),
+                                pa::kQ8MergeThreads, 0, stream, p, L.grid, group, head_dim);
 }

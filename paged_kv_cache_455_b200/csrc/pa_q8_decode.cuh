@@ -45,8 +45,11 @@
 // Work is split as in decode_kernel: every CTA owns an equal, contiguous range
 // of the batch's tiles (mode 0), or whole segments (mode 1); a segment is the
 // run of tiles of one sequence and head group.  The pieces of a segment cut by
-// range borders go to the workspace as fp32 (maximum, sum, accumulator); the
-// CTA whose piece is the last to arrive joins them after its range.
+// range borders go to the workspace as fp32 (maximum, sum, accumulator).  Cut in
+// a few pieces, the CTA whose piece is the last to arrive joins them after its
+// range; cut in many (few long sequences), reading them all would take one SM
+// longer than a launch (16 KB each at ~30 bytes a cycle: 19 pieces 6 us), and
+// q8_merge_kernel joins them on all SMs.
 #pragma once
 
 #include "pa_kernels.cuh"
@@ -67,6 +70,7 @@ struct Q8DecodeParams {
     unsigned long long *counters;   // mode 0: arrivals at the cut segment that starts in a
                                     // CTA's range, a line each (see segment_arrive)
     uint32_t epoch;          // mode 0: tag of this call's counts (never 0)
+    int merge_later;         // mode 0: q8_merge_kernel joins the pieces
     int32_t *dev_status;
     int64_t num_blocks;
     int num_seqs, num_q_heads, num_kv_heads;
@@ -343,6 +347,8 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
     // One thread: counts this CTA's piece of the cut segment [segS, segE) in;
     // whoever completes the count owes the merge.
     auto arrive_piece = [&](int segS, int segE, int b, int hg) {
+        if (p.merge_later)
+            return;
         const int x0 = cta_of(segS, C, total), np = cta_of(segE - 1, C, total) - x0 + 1;
         if (segment_arrive(p.counters + (int64_t)x0 * kLineWords, p.epoch) == np)
             pend_s[segS >= R0 ? 0 : 1] = make_int4(x0, np, b, hg);
@@ -372,7 +378,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                                 : static_cast<const void *>(&tmap_v);
         struct Batch {
             int b, hg, j, ns, n, seg, id;
-            bool active;
+            bool active, early;
         };
         bool ok = true;
         int issued = 0;
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             Q8Walk w = q8_walk_at(R0, p, cbase, lane);
             int seg = 0;
             auto fill = [&](int g) {
-                Batch d = {0, 0, 0, 1, 0, 0, -1, false};
+                Batch d = {0, 0, 0, 1, 0, 0, -1, false, false};
                 int t0 = 0;
 #pragma unroll 1
                 for (int i = 0; i < batch; ++i) {
@@ -402,6 +408,8 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                         t0 = d.j << p.tt_log2;
                         d.n = min(tt, w.ctx - t0);
                         d.active = btok < d.n;
+                        // no row of the sequence's last block
+                        d.early = t0 + tt <= ((w.ctx - 1) & ~(p.block_size - 1));
                     }
                 }
                 // one load for the whole batch, waited for by its first use
@@ -411,21 +419,32 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                 return d;
             };
             Batch cur = fill(R0), nxt;
-            // pools and scales may be written by the kernel ahead
-            ptx::grid_wait_prerequisites();
+            // The kernel ahead may write the last block of every sequence (its
+            // rows and scales): the first tiles up to one with such a block are
+            // fetched before it has completed, the rest after.
+            bool waited = false;
             for (int k0 = 0; ok && k0 < nk; k0 += batch, cur = nxt) {
                 const bool valid = cur.active && cur.id >= 0 && (int64_t)cur.id < p.num_blocks;
                 const int head = cur.hg * hpc + bhead;
                 float ks = 0.f, vs = 0.f;
-                if (valid && !is_k) {
-                    const int64_t at = (int64_t)cur.id * p.num_kv_heads + head;
-                    ks = __ldcg(p.k_scales + at);
-                    vs = __ldcg(p.v_scales + at);
-                }
+                auto load_scales = [&](bool now) {
+                    if (now && valid && !is_k) {
+                        const int64_t at = (int64_t)cur.id * p.num_kv_heads + head;
+                        ks = __ldcg(p.k_scales + at);
+                        vs = __ldcg(p.v_scales + at);
+                    }
+                };
+                load_scales(waited || cur.early);
                 const unsigned vmask = __ballot_sync(kFull, valid);
                 const unsigned bmask = __ballot_sync(kFull, cur.active && !valid);
                 for (int i = 0; i < batch && k0 + i < nk; ++i) {
                     const int k = k0 + i, s = k % S;
+                    if (!waited &&
+                        (k >= S || !__shfl_sync(kFull, (int)cur.early, i << nb_log2))) {
+                        ptx::grid_wait_prerequisites();
+                        waited = true;
+                        load_scales(!cur.early);
+                    }
                     if (__any_sync(kFull, *abort_flag != 0))
                         break;
                     if (k >= S &&
@@ -722,7 +741,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
         ptx::grid_wait_prerequisites();
         // this CTA's counter starts the call at (epoch, 0), unless an arrival
         // has already counted in it
-        if (p.mode == 0 && tid == 0)
+        if (p.mode == 0 && !p.merge_later && tid == 0)
             ptx::red_max_relaxed_gpu_u64(p.counters + (int64_t)blockIdx.x * kLineWords,
                                          (unsigned long long)p.epoch << 32);
         for (int b = blockIdx.x; set == 0 && b < p.num_seqs; b += gridDim.x) {
@@ -1219,5 +1238,111 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
 }
 
 constexpr int kQ8MaxCtas = 148;   // (a merge's weights have room for so many pieces)
+
+// Joins the pieces of every cut segment of a batch of at most 32 sequences:
+// CTA (segment, head, part) sums 128 elements of one head row, warp w taking
+// pieces w, w + 4, ...  Which pieces a segment has follows from the lengths, so
+// that is settled before the decode kernel has completed.
+constexpr int kQ8MergeThreads = 128;
+
+__global__ void __launch_bounds__(kQ8MergeThreads) q8_merge_kernel(const Q8DecodeParams p, int ctas,
+                                                                   int G, int D)
+{
+    constexpr int AHEAD = 6;                             // pieces loaded before their weights
+    __shared__ float wt[kQ8MaxCtas];
+    __shared__ float4 part_s[3][32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    ptx::grid_launch_dependents();
+    const int parts = G * D / 128;
+    const int part = blockIdx.x % parts, rest = blockIdx.x / parts;
+    const int h = rest % p.hpc, seg = rest / p.hpc;
+    const int b = seg / p.head_groups, hg = seg - b * p.head_groups;
+    const int nt = lane < p.num_seqs ? q8_tiles(eff_ctx(p.context_lens[lane], p.ctx_cap), p) : 0;
+    int incl = nt * p.head_groups;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o)
+            incl += v;
+    }
+    const int total = __shfl_sync(kFull, incl, 31);
+    const int mine = __shfl_sync(kFull, nt, b);
+    const int s0 = __shfl_sync(kFull, incl, b) - mine * p.head_groups + hg * mine;
+    const int C = min(ctas, max(total, 1));
+    const int x0 = mine > 0 ? cta_of(s0, C, total) : 0;
+    const int np = mine > 0 ? cta_of(s0 + mine - 1, C, total) - x0 + 1 : 1;
+    const int rows = p.hpc * G, row = h * G + part * 128 / D;
+    const float *first = p.pieces + (int64_t)2 * x0 * p.slot_floats;
+    auto piece = [&](int c) {                            // slots 2 x0 + 1, then 2 (x0 + c)
+        return first + (int64_t)(c == 0 ? 1 : 2 * c) * p.slot_floats;
+    };
+    const int off = h * G * D + part * 128 + 4 * lane;   // of this lane's four elements
+    ptx::grid_wait_prerequisites();
+    if (np == 1)
+        return;                                          // whole, or empty: written already
+    float4 v[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (warp + 4 * i < np)
+            v[i] = __ldcg(reinterpret_cast<const float4 *>(piece(warp + 4 * i) + off));
+    // every warp finds the row's maximum and sum; warp w keeps the weights of
+    // its own pieces
+    const int at = rows * D + 2 * row;
+    float2 ml[(kQ8MaxCtas + 31) / 32];
+    float M = -INFINITY, sum = 0.f, flag = 0.f;
+#pragma unroll
+    for (int i = 0; i < (kQ8MaxCtas + 31) / 32; ++i) {
+        const int c = lane + 32 * i;
+        ml[i] = make_float2(-INFINITY, 0.f);
+        if (c < np) {
+            ml[i] = __ldcg(reinterpret_cast<const float2 *>(piece(c) + at));
+            flag = fmaxf(flag, __ldcg(piece(c) + rows * D + 2 * rows));
+        }
+        M = fmaxf(M, ml[i].x);
+    }
+    M = ptx::warp_max(M);
+#pragma unroll
+    for (int i = 0; i < (kQ8MaxCtas + 31) / 32; ++i) {
+        ml[i].x = ml[i].x == -INFINITY ? 0.f : ptx::ex2(ml[i].x - M);
+        sum += ml[i].x == 0.f ? 0.f : ml[i].y * ml[i].x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(kFull, sum, o);
+    const float inv = sum == 0.f ? 0.f : __frcp_rn(sum);
+    const bool bad = __any_sync(kFull, flag != 0.f);
+    if (flag == 1.f && h == 0 && part == 0 && warp == 0)
+        report(p.dev_status, PA_DEV_BAD_BLOCK);
+#pragma unroll
+    for (int i = 0; i < (kQ8MaxCtas + 31) / 32; ++i)
+        if (lane + 32 * i < np && (lane & 3) == warp)
+            wt[lane + 32 * i] = ml[i].x * inv;
+    __syncwarp();
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4 &x, float f) {
+        a.x = fmaf(x.x, f, a.x);
+        a.y = fmaf(x.y, f, a.y);
+        a.z = fmaf(x.z, f, a.z);
+        a.w = fmaf(x.w, f, a.w);
+    };
+    if (!bad) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (warp + 4 * i < np)
+                add(v[i], wt[warp + 4 * i]);
+#pragma unroll 6
+        for (int c = warp + 4 * AHEAD; c < np; c += 4)
+            add(__ldcg(reinterpret_cast<const float4 *>(piece(c) + off)), wt[c]);
+    }
+    if (warp > 0)
+        part_s[warp - 1][lane] = a;
+    __syncthreads();
+    if (warp > 0)
+        return;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        add(part_s[i][lane], 1.f);
+    store4(p.out + ((int64_t)b * p.num_q_heads + (int64_t)hg * rows) * D + off, a);
+}
 
 }  // namespace pa

@@ -321,10 +321,11 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
     constexpr int UNITS = D / 16;            // threads per row
     constexpr int RPB = 128 / UNITS;         // rows per pass of the CTA
     using V8 = Vec<__nv_bfloat16>;
-    // attention over these pools waits for this grid before it reads pools,
-    // scales or queries, and everything else before it reads what this grid
-    // writes; so the next kernel may start its set-up now
-    pa::ptx::grid_launch_dependents();
+    // With one new token per sequence this grid writes only in each sequence's
+    // last block, of which a decode kernel reads nothing before this grid has
+    // completed: the next kernel may start now.  (A chunk fills more blocks.)
+    if (p.max_q_len == 1)
+        pa::ptx::grid_launch_dependents();
     pa::ptx::grid_wait_prerequisites();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int u = tid % UNITS, rl = tid / UNITS;
