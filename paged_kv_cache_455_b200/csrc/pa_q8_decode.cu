@@ -22,7 +22,7 @@ template <int D, int G>
 pa_status run(Launch &L, bool launch)
 {
     auto fn = &pa::q8_decode_kernel<D, G>;
-    const int smem = pa::Q8Smem<D, G>::bytes + 4 * (L.chunks + 1);
+    const int smem = pa::Q8Smem<D, G>::bytes + 8 * (L.chunks + 1);
     int cap = 0;
     const pa_status st = pa::grid_capacity(reinterpret_cast<const void *>(fn), pa::Q8Smem<D, G>::kThreads,
                                            smem, &cap);
@@ -66,7 +66,7 @@ extern "C" pa_status pa_decode_attention_q8(void *out, const void *query, const 
                                             void *stream)
 {
     if ((head_dim != 128 && head_dim != 256) || (block_size != 16 && block_size != 32) ||
-        num_seqs > 32 * pa::kMaxChunks)
+        num_seqs > pa::kQ8MaxSeqs)
         return PA_ERR_UNSUPPORTED;
     int group = 0, bs_log2 = 0;
     pa_status st = pa::check_attention(out, query, k_pool, v_pool, block_tables,
@@ -103,6 +103,8 @@ extern "C" pa_status pa_decode_attention_q8(void *out, const void *query, const 
     p.box_log2 = block_size == 32 ? 5 : 4;
     p.head_groups = num_kv_heads / p.hpc;
     p.scale_log2 = scale * pa::kLog2e;
+    // a segment's end takes ~2 us, a tile's bytes 1.5 us (d 256) or 0.75 us
+    p.end_tiles = head_dim == 256 ? 1 : 3;
     const unsigned long long wait_ns = pa::test_wait_ns();
     p.wait_ns = wait_ns ? wait_ns : pa::kWaitLimitNs;
     p.withhold_cta = pa::test_withhold_cta();

@@ -42,9 +42,12 @@
 // and references of its own; they are joined at the segment's end.  With
 // d = 256 and G = 8 tensor memory holds one set's accumulators only.
 //
-// Work is split as in decode_kernel: every CTA owns an equal, contiguous range
-// of the batch's tiles (mode 0), or whole segments (mode 1); a segment is the
-// run of tiles of one sequence and head group.  The pieces of a segment cut by
+// Work is split as in decode_kernel: every CTA owns a contiguous range of the
+// batch's tiles (mode 0), or whole segments (mode 1); a segment is the run of
+// tiles of one sequence and head group.  The ranges are equal in the time they
+// take: a segment's end costs a CTA about as much as end_tiles more tiles (its
+// accumulators have to be read out before the next segment's products), so
+// ranges are equal shares of the tiles plus end_tiles for every segment.  The pieces of a segment cut by
 // range borders go to the workspace as fp32 (maximum, sum, accumulator).  Cut in
 // a few pieces, the CTA whose piece is the last to arrive joins them after its
 // range; cut in many (few long sequences), reading them all would take one SM
@@ -58,6 +61,7 @@
 namespace pa {
 
 constexpr int kQ8Tile = 128;              // rows of K and V per tile (MMA M)
+constexpr int kQ8MaxSeqs = 16384;         // (the prefix of the tile counts is in shared memory)
 constexpr int kQ8SmemStages = 6 * 32768;  // bytes of the stage ring
 constexpr float kQ8Grow = 15.f;           // log2 growth that makes a rescale
 
@@ -82,6 +86,7 @@ struct Q8DecodeParams {
     int head_groups;
     int mode;                // 0: equal ranges, 1: whole segments
     int slot_floats;
+    int end_tiles;           // tiles that a segment's end is counted as
     float scale_log2;
     uint64_t wait_ns;
     int withhold_cta;        // test hook, as in DecodeParams
@@ -130,7 +135,7 @@ struct Q8Smem {
     static constexpr int cbase_off = flag_off + 16;
     // (the prefix of the tile counts comes last, as long as the batch needs)
     static constexpr int bytes = 1024 + cbase_off;
-    static_assert(bytes + 4 * (kMaxChunks + 1) <= kSmemBudget, "shared memory per CTA");
+    static_assert(bytes + 8 * (kQ8MaxSeqs / 32 + 1) <= kSmemBudget, "shared memory per CTA");
 };
 
 // Position in the batch's sequence of segments (whole warp, uniform).
@@ -138,6 +143,7 @@ struct Q8Walk {
     int b, hg;       // sequence, head group
     int ctx, nt;     // its effective length, tiles of the segment
     int g0;          // global index of the segment's first tile
+    int ord;         // ordinal of the segment in the batch
 };
 
 __device__ __forceinline__ int q8_tiles(int ctx, const Q8DecodeParams &p)
@@ -145,69 +151,90 @@ __device__ __forceinline__ int q8_tiles(int ctx, const Q8DecodeParams &p)
     return (ctx + (1 << p.tt_log2) - 1) >> p.tt_log2;
 }
 
-// cbase[c] = global index of the first tile of sequence 32 c; returns the
-// total.  Every thread of the CTA.
-__device__ __forceinline__ int q8_prefix(const Q8DecodeParams &p, int *cbase)
+// For chunk c of 32 sequences, cbase[2 c] = tiles and cbase[2 c + 1] = segments
+// before it; the totals come last.  Every thread of the CTA.
+__device__ __forceinline__ void q8_prefix(const Q8DecodeParams &p, int *cbase)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
     const int nch = (p.num_seqs + 31) >> 5;
     for (int c = warp; c < nch; c += nwarps) {
         const int b = c * 32 + lane;
-        int t = b < p.num_seqs ? q8_tiles(eff_ctx(p.context_lens[b], p.ctx_cap), p) * p.head_groups
-                               : 0;
+        int t = b < p.num_seqs ? q8_tiles(eff_ctx(p.context_lens[b], p.ctx_cap), p) : 0;
+        const int n = __popc(__ballot_sync(kFull, t > 0));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             t += __shfl_xor_sync(kFull, t, o);
-        if (lane == 0)
-            cbase[c + 1] = t;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int carry = 0;
-        if (lane == 0)
-            cbase[0] = 0;
-        for (int c0 = 0; c0 < nch; c0 += 32) {
-            const int c = c0 + lane;
-            int v = c < nch ? cbase[c + 1] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(kFull, v, o);
-                if (lane >= o)
-                    v += u;
-            }
-            if (c < nch)
-                cbase[c + 1] = carry + v;
-            carry += __shfl_sync(kFull, v, 31);
+        if (lane == 0) {
+            cbase[2 * c + 2] = t * p.head_groups;
+            cbase[2 * c + 3] = n * p.head_groups;
         }
     }
     __syncthreads();
-    return cbase[nch];
+    if (warp == 0) {
+        int ct = 0, cn = 0;
+        if (lane < 2)
+            cbase[lane] = 0;
+        for (int c0 = 0; c0 < nch; c0 += 32) {
+            const int c = c0 + lane;
+            int t = c < nch ? cbase[2 * c + 2] : 0, n = c < nch ? cbase[2 * c + 3] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(kFull, t, o), v = __shfl_up_sync(kFull, n, o);
+                if (lane >= o) {
+                    t += u;
+                    n += v;
+                }
+            }
+            if (c < nch) {
+                cbase[2 * c + 2] = ct + t;
+                cbase[2 * c + 3] = cn + n;
+            }
+            ct += __shfl_sync(kFull, t, 31);
+            cn += __shfl_sync(kFull, n, 31);
+        }
+    }
+    __syncthreads();
 }
 
-// The segment holding tile g (below the total).
-__device__ __forceinline__ Q8Walk q8_walk_at(int g, const Q8DecodeParams &p, const int *cbase,
-                                             int lane)
+// The segment holding tile g, or with `weight` > 0 the one holding unit g of
+// the sequence in which every segment is its tiles and then `weight` units
+// (g below the total).
+__device__ __forceinline__ Q8Walk q8_walk_at(int g, int weight, const Q8DecodeParams &p,
+                                             const int *cbase, int lane)
 {
-    const int c = chunk_of(cbase, (p.num_seqs + 31) >> 5, g);
+    int c = 0, hi = ((p.num_seqs + 31) >> 5) - 1;        // the last chunk that starts at or before g
+    while (c < hi) {
+        const int mid = (c + hi + 1) >> 1;
+        if (cbase[2 * mid] + weight * cbase[2 * mid + 1] <= g)
+            c = mid;
+        else
+            hi = mid - 1;
+    }
     const int b = c * 32 + lane;
     const int ctx = b < p.num_seqs ? eff_ctx(p.context_lens[b], p.ctx_cap) : 0;
     const int nt = q8_tiles(ctx, p);
-    int incl = nt * p.head_groups;
+    int t = nt * p.head_groups;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(kFull, incl, o);
+        const int u = __shfl_up_sync(kFull, t, o);
         if (lane >= o)
-            incl += u;
+            t += u;
     }
-    const unsigned past = __ballot_sync(kFull, cbase[c] + incl > g);
+    const unsigned some = __ballot_sync(kFull, nt > 0);
+    const int n = __popc(some & (0xffffffffu >> (31 - lane))) * p.head_groups;
+    const int t0 = cbase[2 * c] + t - nt * p.head_groups;            // before this sequence
+    const int n0 = cbase[2 * c + 1] + n - (nt > 0 ? p.head_groups : 0);
+    const unsigned past = __ballot_sync(
+        kFull, nt > 0 && t0 + weight * n0 + (nt + weight) * p.head_groups > g);
     const int src = past ? __ffs(past) - 1 : 31;
     Q8Walk w;
     w.b = c * 32 + src;
     w.ctx = __shfl_sync(kFull, ctx, src);
     w.nt = max(__shfl_sync(kFull, nt, src), 1);
-    const int start = cbase[c] + __shfl_sync(kFull, incl - nt * p.head_groups, src);
-    w.hg = (g - start) / w.nt;
-    w.g0 = start + w.hg * w.nt;
+    const int st = __shfl_sync(kFull, t0, src), sn = __shfl_sync(kFull, n0, src);
+    w.hg = (g - st - weight * sn) / (w.nt + weight);
+    w.g0 = st + w.hg * w.nt;
+    w.ord = sn + w.hg;
     return w;
 }
 
@@ -215,6 +242,7 @@ __device__ __forceinline__ Q8Walk q8_walk_at(int g, const Q8DecodeParams &p, con
 __device__ __forceinline__ void q8_walk_next(Q8Walk &w, const Q8DecodeParams &p, int lane)
 {
     w.g0 += w.nt;
+    ++w.ord;
     if (++w.hg < p.head_groups)
         return;
     w.hg = 0;
@@ -232,16 +260,19 @@ __device__ __forceinline__ void q8_walk_next(Q8Walk &w, const Q8DecodeParams &p,
     }
 }
 
-__device__ __forceinline__ int q8_range_begin(int x, int C, int T, const Q8DecodeParams &p,
-                                              const int *cbase, int lane)
+// First tile of CTA x's range: of the `units` (tiles and segment ends), CTA x
+// has [x units / C, (x + 1) units / C), and of those the tiles.
+__device__ __forceinline__ int q8_range_begin(int x, int C, int T, int units,
+                                              const Q8DecodeParams &p, const int *cbase, int lane)
 {
-    if (x >= C)
+    const int v = (int)((int64_t)x * units / C);
+    if (x >= C || v >= units)
         return T;
-    const int g = (int)((int64_t)x * T / C);
-    if (p.mode == 0 || g >= T)
-        return g;
-    const Q8Walk w = q8_walk_at(g, p, cbase, lane);
-    return w.g0 == g ? g : w.g0 + w.nt;
+    const Q8Walk w = q8_walk_at(v, p.end_tiles, p, cbase, lane);
+    const int into = v - (w.g0 + p.end_tiles * w.ord);   // units into the segment
+    if (p.mode == 0)
+        return w.g0 + min(into, w.nt);
+    return into == 0 ? w.g0 : w.g0 + w.nt;               // whole segments
 }
 
 // Two fp32 values to E5M2 codes, `lo` in byte 0 (nearest, ties to even).
@@ -324,13 +355,15 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
     }
     ptx::tc_fence_before();
     // lengths and block tables are read before the kernel ahead has completed
-    const int total = q8_prefix(p, cbase);              // contains __syncthreads
+    q8_prefix(p, cbase);                                // contains __syncthreads
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     const uint32_t o_tm = tmem + 128;
+    const int *totals = cbase + 2 * ((p.num_seqs + 31) >> 5);
+    const int total = totals[0], units = total + p.end_tiles * totals[1];
     const int C = min((int)gridDim.x, max(total, 1));
-    const int R0 = q8_range_begin(blockIdx.x, C, total, p, cbase, lane);
-    const int R1 = q8_range_begin(blockIdx.x + 1, C, total, p, cbase, lane);
+    const int R0 = q8_range_begin(blockIdx.x, C, total, units, p, cbase, lane);
+    const int R1 = q8_range_begin(blockIdx.x + 1, C, total, units, p, cbase, lane);
     const int nk = R1 - R0;
     if (tid == 0)
         ptx::grid_launch_dependents();
@@ -344,12 +377,14 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             return false;
         return __all_sync(kFull, ptx::mbar_wait_bounded(bar, parity, lim));
     };
-    // One thread: counts this CTA's piece of the cut segment [segS, segE) in;
-    // whoever completes the count owes the merge.
-    auto arrive_piece = [&](int segS, int segE, int b, int hg) {
+    // One thread: counts this CTA's piece of the cut segment [segS, segE), the
+    // ord-th of the batch, in; whoever completes the count owes the merge.
+    auto arrive_piece = [&](int segS, int segE, int ord, int b, int hg) {
         if (p.merge_later)
             return;
-        const int x0 = cta_of(segS, C, total), np = cta_of(segE - 1, C, total) - x0 + 1;
+        const int before = p.end_tiles * ord;
+        const int x0 = cta_of(segS + before, C, units);
+        const int np = cta_of(segE - 1 + before, C, units) - x0 + 1;
         if (segment_arrive(p.counters + (int64_t)x0 * kLineWords, p.epoch) == np)
             pend_s[segS >= R0 ? 0 : 1] = make_int4(x0, np, b, hg);
     };
@@ -386,7 +421,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             if (lane == 0)
                 ptx::prefetch_tensormap(tmap);
             const uint64_t policy = ptx::policy_evict_first();
-            Q8Walk w = q8_walk_at(R0, p, cbase, lane);
+            Q8Walk w = q8_walk_at(R0, 0, p, cbase, lane);
             int seg = 0;
             auto fill = [&](int g) {
                 Batch d = {0, 0, 0, 1, 0, 0, -1, false, false};
@@ -614,7 +649,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
         bool ok = true;
         if (nk > 0) {
             constexpr int E = D / 32;                    // elements per lane
-            Q8Walk w = q8_walk_at(R0, p, cbase, lane);
+            Q8Walk w = q8_walk_at(R0, 0, p, cbase, lane);
             for (int seg = 0; w.g0 < R1; ++seg) {
                 const int qb = seg % QB;
                 if (__any_sync(kFull, *abort_flag != 0))
@@ -762,6 +797,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
         float m[G], l[G], fac[G];
         bool fail = false, seg_bad = false;
         int exchanges = 0;
+        const int ord0 = nk > 0 ? q8_walk_at(R0, 0, p, cbase, lane).ord : 0;
         auto wait = [&](uint32_t bar, uint32_t parity) {
             if (!fail && !ready(bar, parity)) {
                 fail = true;
@@ -1116,7 +1152,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                 if (ptx::barrier_or(bar0, 128, false))
                     break;                                    // (never)
                 if (st == 0)
-                    arrive_piece(segS, segE, mb, mhg);
+                    arrive_piece(segS, segE, ord0 + seg, mb, mhg);
             } else if (seg_bad && st == 0) {
                 report(p.dev_status, PA_DEV_BAD_BLOCK);
             }
@@ -1134,7 +1170,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
         // a wait ran out: zeros for the segments that are not complete, and a
         // mark in their pieces
         const int rows = hpc * G;
-        Q8Walk w = q8_walk_at(R0 + *tiles_done, p, cbase, lane);
+        Q8Walk w = q8_walk_at(R0 + *tiles_done, 0, p, cbase, lane);
         while (true) {
             const int segE = w.g0 + w.nt;
             if (w.g0 >= R0 && segE <= R1) {
@@ -1144,7 +1180,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             } else if (tid == 0) {
                 float *ps = p.pieces + (int64_t)(2 * blockIdx.x + (w.g0 >= R0 ? 1 : 0)) * p.slot_floats;
                 ps[rows * D + 2 * rows] = 2.f;
-                arrive_piece(w.g0, segE, w.b, w.hg);
+                arrive_piece(w.g0, segE, w.ord, w.b, w.hg);
             }
             if (segE >= R1)
                 break;
@@ -1258,19 +1294,22 @@ __global__ void __launch_bounds__(kQ8MergeThreads) q8_merge_kernel(const Q8Decod
     const int h = rest % p.hpc, seg = rest / p.hpc;
     const int b = seg / p.head_groups, hg = seg - b * p.head_groups;
     const int nt = lane < p.num_seqs ? q8_tiles(eff_ctx(p.context_lens[lane], p.ctx_cap), p) : 0;
-    int incl = nt * p.head_groups;
+    // units (see q8_range_begin) up to and with sequence `lane`
+    const int size = nt > 0 ? (nt + p.end_tiles) * p.head_groups : 0;
+    int incl = size, tiles = nt * p.head_groups;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(kFull, incl, o);
         if (lane >= o)
             incl += v;
+        tiles += __shfl_xor_sync(kFull, tiles, o);
     }
-    const int total = __shfl_sync(kFull, incl, 31);
+    const int units = __shfl_sync(kFull, incl, 31);
     const int mine = __shfl_sync(kFull, nt, b);
-    const int s0 = __shfl_sync(kFull, incl, b) - mine * p.head_groups + hg * mine;
-    const int C = min(ctas, max(total, 1));
-    const int x0 = mine > 0 ? cta_of(s0, C, total) : 0;
-    const int np = mine > 0 ? cta_of(s0 + mine - 1, C, total) - x0 + 1 : 1;
+    const int s0 = __shfl_sync(kFull, incl - size, b) + hg * (mine + p.end_tiles);
+    const int C = min(ctas, max(tiles, 1));
+    const int x0 = mine > 0 ? cta_of(s0, C, units) : 0;
+    const int np = mine > 0 ? cta_of(s0 + mine - 1, C, units) - x0 + 1 : 1;
     const int rows = p.hpc * G, row = h * G + part * 128 / D;
     const float *first = p.pieces + (int64_t)2 * x0 * p.slot_floats;
     auto piece = [&](int c) {                            // slots 2 x0 + 1, then 2 (x0 + c)

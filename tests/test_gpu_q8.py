@@ -300,10 +300,10 @@ def test_decode_wait_that_runs_out(pa, cta):
         pa.testing_withhold_copy(-1)
         pa.testing_set_wait_limit_ns(0)
     assert int(status.item()) == pa.PA_DEV_WAIT_TIMEOUT
+    # (a range is an equal share of every sequence's tiles and one unit more)
     tiles = -(-3000 // 32)
-    total = 12 * tiles
-    r0, r1 = cta * total // 148, (cta + 1) * total // 148
-    lost = {t // tiles for t in range(r0, r1)}
+    r0, r1 = (x * 12 * (tiles + 1) // 148 for x in (cta, cta + 1))
+    lost = {v // (tiles + 1) for v in range(r0, r1) if v % (tiles + 1) < tiles}
     for b in range(12):
         assert (out[b] == 0).all() if b in lost else torch.equal(out[b], want[b])
     assert torch.equal(c.decode(pa, ws=ws), want)

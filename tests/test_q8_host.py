@@ -95,7 +95,7 @@ ATTENTION = [
 ]
 
 
-@pytest.mark.parametrize("kw,want", ATTENTION + [(dict(B=32769), 2)])
+@pytest.mark.parametrize("kw,want", ATTENTION + [(dict(B=16385), 2)])
 def test_decode_refusals(pa, kw, want):
     assert _decode(pa, **kw) == want
 
