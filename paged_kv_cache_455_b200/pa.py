@@ -111,8 +111,15 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without building a torch.cuda.Stream around it
+# (10 us of a call, more than most of these kernels take).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -381,14 +388,30 @@ def rope_table(max_position: int, rot_dim: int, base: float = 10000.0, device="c
     return torch.cat([ang.cos(), ang.sin()], dim=1).float().contiguous()
 
 
-def _token_rows(t: torch.Tensor, name: str, total: int, d: int, dtype) -> int:
-    """Elements between tokens of t [total, heads, d], whose heads are dense."""
-    if not t.is_cuda or t.dim() != 3 or t.shape[0] != total or t.shape[2] != d or t.dtype != dtype:
-        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, {d}] of {dtype}")
-    heads = t.shape[1]
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+# (None where torch has no CUDA: then no tensor passes _dense)
+_current_device = getattr(torch._C, "_cuda_getDevice", lambda: None)
+
+
+def _dense(*tensors) -> None:
+    """Contiguous CUDA tensors of the current device (the one launched on)."""
+    dev = _current_device() if tensors[0].is_cuda else None
+    for t in tensors:
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous CUDA tensors of the current device")
+
+
+def _token_rows(t: torch.Tensor, name: str, T: int, d: int, dtype) -> int:
+    """Elements between tokens of t [T, heads, d], whose heads are dense."""
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != d or t.dtype != dtype or not t.is_cuda or \
+            t.get_device() != _current_device():
+        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, {d}] of {dtype} "
+                         "on the current device")
+    heads = shape[1]
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and heads > 1):
         raise ValueError(f"the heads of {name} must be dense")
-    return t.stride(0) if total > 1 else max(heads, 1) * d
+    return s0 if T > 1 else max(heads, 1) * d
 
 
 def _rope_args(query_out, query, key, value, positions, cos_sin, dtype):
@@ -399,29 +422,32 @@ def _rope_args(query_out, query, key, value, positions, cos_sin, dtype):
     T, hkv, d = key.shape
     ks = _token_rows(key, "key", T, d, dtype)
     vs = _token_rows(value, "value", T, d, dtype)
-    if value.shape != key.shape:
+    if value.shape[1] != hkv:
         raise ValueError("shape mismatch")
     hq = qs = qos = 0
-    if (query is None) != (query_out is None):
-        raise ValueError("query and query_out go together")
-    if query is not None:
+    qp = qop = None
+    if query is not None and query_out is not None:
         qs = _token_rows(query, "query", T, d, dtype)
         qos = _token_rows(query_out, "query_out", T, d, dtype)
-        if query_out.shape != query.shape:
-            raise ValueError("shape mismatch")
         hq = query.shape[1]
-    rot = max_pos = 0
-    if cos_sin is not None:
-        _cuda(cos_sin, positions)
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be float32 [max_position, rot_dim]")
+        if query_out.shape[1] != hq:
+            raise ValueError("shape mismatch")
+        qp, qop = query.data_ptr(), query_out.data_ptr()
+    elif query is not query_out:
+        raise ValueError("query and query_out go together")
+    if cos_sin is None:
+        if positions is not None:
+            raise ValueError("positions need cos_sin")
+        rot = (None, None, 0, 0)
+    else:
         if positions is None or positions.dtype != torch.int64 or positions.shape != (T,):
             raise ValueError("positions must be int64 [tokens]")
-        max_pos, rot = cos_sin.shape
-    elif positions is not None:
-        raise ValueError("positions need cos_sin")
-    rows = (_ptr(query_out), qos, _ptr(query), qs, _ptr(key), ks, _ptr(value), vs)
-    return rows, (_ptr(positions), _ptr(cos_sin), rot, max_pos), (T, hq, hkv, d)
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be float32 [max_position, rot_dim]")
+        _dense(cos_sin, positions)
+        max_pos, r = cos_sin.shape
+        rot = (positions.data_ptr(), cos_sin.data_ptr(), r, max_pos)
+    return (qop, qos, qp, qs, key.data_ptr(), ks, value.data_ptr(), vs), rot, (T, hq, hkv, d)
 
 
 def pa_rope_and_cache(query_out: Optional[torch.Tensor], query: Optional[torch.Tensor],
@@ -434,39 +460,45 @@ def pa_rope_and_cache(query_out: Optional[torch.Tensor], query: Optional[torch.T
     key/value [T, Hkv, d], tokens at any stride; pools [nb, bs, Hkv, d];
     slot_mapping, positions [T] int64; cos_sin [max_position, rot_dim] fp32
     (None: nothing is rotated)."""
-    _cuda(k_pool, v_pool, slot_mapping, dev_status)
+    dtype = k_pool.dtype
     rows, rot, (T, hq, hkv, d) = _rope_args(query_out, query, key, value, positions, cos_sin,
-                                            k_pool.dtype)
-    nb, bs = k_pool.shape[:2]
-    if v_pool.shape != k_pool.shape or v_pool.dtype != k_pool.dtype or \
-            k_pool.shape[2:] != (hkv, d):
+                                            dtype)
+    _dense(k_pool, v_pool, slot_mapping)
+    if dev_status is not None:
+        _dense(dev_status)
+    shape = k_pool.shape
+    if len(shape) != 4 or v_pool.shape != shape or v_pool.dtype != dtype or shape[2:] != (hkv, d):
         raise ValueError("pool mismatch")
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be int64 [T]")
-    _check(lib.pa_rope_and_cache(*rows, _ptr(k_pool), _ptr(v_pool), _ptr(slot_mapping), *rot,
-                                 int(bool(interleaved)), T, hq, hkv, d, bs, nb,
-                                 _dtype_code(k_pool), _ptr(dev_status), _stream(stream)),
-           "pa_rope_and_cache")
+    _check(lib.pa_rope_and_cache(*rows, k_pool.data_ptr(), v_pool.data_ptr(),
+                                 slot_mapping.data_ptr(), *rot, 1 if interleaved else 0, T, hq,
+                                 hkv, d, shape[1], shape[0], _dtype_code(k_pool),
+                                 _ptr(dev_status), _stream(stream)), "pa_rope_and_cache")
 
 
 def _q8_pools(k_pool, v_pool, k_scales, v_scales):
     """Checks one side's block-scaled pools; returns (nb, bs, hkv, d)."""
-    if k_pool.dim() != 4 or v_pool.shape != k_pool.shape:
+    shape = k_pool.shape
+    if len(shape) != 4 or v_pool.shape != shape:
         raise ValueError("pools must be [nb, bs, Hkv, d]")
     if k_pool.dtype not in FP8_POOL_DTYPES or v_pool.dtype not in FP8_POOL_DTYPES:
         raise ValueError("pools must hold E4M3 codes (uint8 or float8_e4m3fn)")
-    nb, bs, hkv, d = k_pool.shape
-    for s in (k_scales, v_scales):
-        if s.dtype != torch.float32 or s.shape != (nb, hkv):
-            raise ValueError("scales must be float32 [nb, Hkv]")
-    return nb, bs, hkv, d
+    want = (shape[0], shape[2])
+    if k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32 or \
+            k_scales.shape != want or v_scales.shape != want:
+        raise ValueError("scales must be float32 [nb, Hkv]")
+    return shape
 
 
-def _tables(block_tables, context_lens, B):
-    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != B:
+def _tables(block_tables, context_lens, B) -> int:
+    """Checks the tables of B sequences; returns their width."""
+    shape = block_tables.shape
+    if block_tables.dtype != torch.int32 or len(shape) != 2 or shape[0] != B:
         raise ValueError("block_tables must be int32 [B, max_blocks]")
     if context_lens.dtype != torch.int32 or context_lens.shape != (B,):
         raise ValueError("context_lens must be int32 [B]")
+    return shape[1]
 
 
 def pa_rope_and_cache_q8(query_out: Optional[torch.Tensor], query: Optional[torch.Tensor],
@@ -481,20 +513,23 @@ def pa_rope_and_cache_q8(query_out: Optional[torch.Tensor], query: Optional[torc
     cu_q_lens[b] .. cu_q_lens[b + 1] - 1, the last of its context_lens[b]
     cached tokens.  cu_q_lens [B + 1], block_tables [B, max_blocks],
     context_lens [B] int32."""
-    _cuda(k_pool, v_pool, k_scales, v_scales, cu_q_lens, block_tables, context_lens, dev_status)
     rows, rot, (T, hq, hkv, d) = _rope_args(query_out, query, key, value, positions, cos_sin,
                                             torch.bfloat16)
+    _dense(k_pool, v_pool, k_scales, v_scales, cu_q_lens, block_tables, context_lens)
+    if dev_status is not None:
+        _dense(dev_status)
     nb, bs, phkv, pd = _q8_pools(k_pool, v_pool, k_scales, v_scales)
-    if (phkv, pd) != (hkv, d):
+    if phkv != hkv or pd != d:
         raise ValueError("pool mismatch")
     B = context_lens.shape[0]
-    _tables(block_tables, context_lens, B)
+    width = _tables(block_tables, context_lens, B)
     if cu_q_lens.dtype != torch.int32 or cu_q_lens.shape != (B + 1,):
         raise ValueError("cu_q_lens must be int32 [B + 1]")
-    _check(lib.pa_rope_and_cache_q8(*rows, _ptr(k_pool), _ptr(v_pool), _ptr(k_scales),
-                                    _ptr(v_scales), _ptr(cu_q_lens), T, int(max_q_len),
-                                    _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
-                                    B, *rot, int(bool(interleaved)), hq, hkv, d, bs, nb,
+    _check(lib.pa_rope_and_cache_q8(*rows, k_pool.data_ptr(), v_pool.data_ptr(),
+                                    k_scales.data_ptr(), v_scales.data_ptr(),
+                                    cu_q_lens.data_ptr(), T, int(max_q_len),
+                                    block_tables.data_ptr(), width, context_lens.data_ptr(), B,
+                                    *rot, 1 if interleaved else 0, hq, hkv, d, bs, nb,
                                     _ptr(dev_status), _stream(stream)), "pa_rope_and_cache_q8")
 
 
@@ -507,21 +542,25 @@ def pa_decode_attention_q8(out: torch.Tensor, query: torch.Tensor, k_pool: torch
     """out, query [B, Hq, d] bf16; pools [nb, bs, Hkv, d] of E4M3 codes with
     scales [nb, Hkv] fp32; block_tables [B, max_blocks], context_lens [B]
     int32; workspace as in pa_decode_attention."""
-    _cuda(out, query, k_pool, v_pool, k_scales, v_scales, block_tables, context_lens, workspace,
-          dev_status)
+    _dense(out, query, k_pool, v_pool, k_scales, v_scales, block_tables, context_lens)
     B, hq, d = query.shape
     nb, bs, hkv, pd = _q8_pools(k_pool, v_pool, k_scales, v_scales)
     if out.shape != query.shape or pd != d:
         raise ValueError("shape mismatch")
     if query.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
         raise ValueError("query and out must be bf16")
-    _tables(block_tables, context_lens, B)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib.pa_decode_attention_q8(_ptr(out), _ptr(query), _ptr(k_pool), _ptr(v_pool),
-                                      _ptr(k_scales), _ptr(v_scales), _ptr(block_tables),
-                                      block_tables.shape[1], _ptr(context_lens), B,
-                                      int(max_context_len), hq, hkv, d, bs, nb, float(scale),
-                                      _ptr(workspace), ws_bytes, _ptr(dev_status),
+    width = _tables(block_tables, context_lens, B)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        _dense(workspace)
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    if dev_status is not None:
+        _dense(dev_status)
+    _check(lib.pa_decode_attention_q8(out.data_ptr(), query.data_ptr(), k_pool.data_ptr(),
+                                      v_pool.data_ptr(), k_scales.data_ptr(),
+                                      v_scales.data_ptr(), block_tables.data_ptr(), width,
+                                      context_lens.data_ptr(), B, int(max_context_len), hq, hkv,
+                                      d, bs, nb, float(scale), ws, ws_bytes, _ptr(dev_status),
                                       _stream(stream)), "pa_decode_attention_q8")
 
 
@@ -533,8 +572,9 @@ def pa_prefill_attention_q8(out: torch.Tensor, query: torch.Tensor, cu_q_lens: t
                             dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """query/out [total_q, Hq, d] bf16; cu_q_lens [B + 1] int32; pools, scales,
     tables and lengths as in pa_decode_attention_q8."""
-    _cuda(out, query, cu_q_lens, k_pool, v_pool, k_scales, v_scales, block_tables, context_lens,
-          dev_status)
+    _dense(out, query, cu_q_lens, k_pool, v_pool, k_scales, v_scales, block_tables, context_lens)
+    if dev_status is not None:
+        _dense(dev_status)
     total_q, hq, d = query.shape
     nb, bs, hkv, pd = _q8_pools(k_pool, v_pool, k_scales, v_scales)
     B = context_lens.shape[0]
@@ -542,16 +582,16 @@ def pa_prefill_attention_q8(out: torch.Tensor, query: torch.Tensor, cu_q_lens: t
         raise ValueError("shape mismatch")
     if query.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
         raise ValueError("query and out must be bf16")
-    _tables(block_tables, context_lens, B)
+    width = _tables(block_tables, context_lens, B)
     if cu_q_lens.dtype != torch.int32 or cu_q_lens.shape != (B + 1,):
         raise ValueError("cu_q_lens must be int32 [B + 1]")
-    _check(lib.pa_prefill_attention_q8(_ptr(out), _ptr(query), _ptr(cu_q_lens), total_q,
-                                       int(max_q_len), _ptr(k_pool), _ptr(v_pool),
-                                       _ptr(k_scales), _ptr(v_scales), _ptr(block_tables),
-                                       block_tables.shape[1], _ptr(context_lens), B,
-                                       int(max_context_len), hq, hkv, d, bs, nb, float(scale),
-                                       _ptr(dev_status), _stream(stream)),
-           "pa_prefill_attention_q8")
+    _check(lib.pa_prefill_attention_q8(out.data_ptr(), query.data_ptr(), cu_q_lens.data_ptr(),
+                                       total_q, int(max_q_len), k_pool.data_ptr(),
+                                       v_pool.data_ptr(), k_scales.data_ptr(),
+                                       v_scales.data_ptr(), block_tables.data_ptr(), width,
+                                       context_lens.data_ptr(), B, int(max_context_len), hq, hkv,
+                                       d, bs, nb, float(scale), _ptr(dev_status),
+                                       _stream(stream)), "pa_prefill_attention_q8")
 
 
 def pa_copy_blocks_q8(dst_k: torch.Tensor, dst_v: torch.Tensor, dst_k_scales: torch.Tensor,
@@ -565,18 +605,22 @@ def pa_copy_blocks_q8(dst_k: torch.Tensor, dst_v: torch.Tensor, dst_k_scales: to
     for t in (dst_k, dst_v, dst_k_scales, dst_v_scales, src_k, src_v, src_k_scales, src_v_scales):
         if not t.is_contiguous() or not (t.is_cuda or t.is_pinned()):
             raise ValueError("pools and scales must be contiguous CUDA or pinned host tensors")
-    _cuda(block_mapping, dev_status)
+    _dense(block_mapping)
+    if dev_status is not None:
+        _dense(dev_status)
     dnb, bs, hkv, d = _q8_pools(dst_k, dst_v, dst_k_scales, dst_v_scales)
-    snb, *same = _q8_pools(src_k, src_v, src_k_scales, src_v_scales)
-    if same != [bs, hkv, d]:
+    shape = _q8_pools(src_k, src_v, src_k_scales, src_v_scales)
+    if shape[1:] != (bs, hkv, d):
         raise ValueError("pool shape mismatch")
-    if block_mapping.dtype != torch.int64 or block_mapping.dim() != 2 or block_mapping.shape[1] != 2:
+    pairs = block_mapping.shape
+    if block_mapping.dtype != torch.int64 or len(pairs) != 2 or pairs[1] != 2:
         raise ValueError("block_mapping must be int64 [P, 2]")
-    _check(lib.pa_copy_blocks_q8(_ptr(dst_k), _ptr(dst_v), _ptr(dst_k_scales), _ptr(dst_v_scales),
-                                 dnb, _ptr(src_k), _ptr(src_v), _ptr(src_k_scales),
-                                 _ptr(src_v_scales), snb, _ptr(block_mapping),
-                                 block_mapping.shape[0], bs, hkv, d, _ptr(dev_status),
-                                 _stream(stream)), "pa_copy_blocks_q8")
+    _check(lib.pa_copy_blocks_q8(dst_k.data_ptr(), dst_v.data_ptr(), dst_k_scales.data_ptr(),
+                                 dst_v_scales.data_ptr(), dnb, src_k.data_ptr(),
+                                 src_v.data_ptr(), src_k_scales.data_ptr(),
+                                 src_v_scales.data_ptr(), shape[0], block_mapping.data_ptr(),
+                                 pairs[0], bs, hkv, d, _ptr(dev_status), _stream(stream)),
+           "pa_copy_blocks_q8")
 
 
 __all__ = [
