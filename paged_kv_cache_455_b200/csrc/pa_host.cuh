@@ -51,23 +51,35 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 // Launches `kernel` as a programmatic dependent of the kernel ahead on the
 // stream; the kernel must execute griddepcontrol.wait in every CTA.
+// With `cluster` > 1 that many consecutive CTAs form a cluster.
 template <typename... KArgs, typename... Args>
-inline pa_status launch_dependent(void (*kernel)(KArgs...), unsigned grid, unsigned threads,
-                                  size_t smem, void *stream, Args... args)
+inline pa_status launch_clusters(void (*kernel)(KArgs...), unsigned cluster, unsigned grid,
+                                 unsigned threads, size_t smem, void *stream, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     count_launch();
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <typename... KArgs, typename... Args>
+inline pa_status launch_dependent(void (*kernel)(KArgs...), unsigned grid, unsigned threads,
+                                  size_t smem, void *stream, Args... args)
+{
+    return launch_clusters(kernel, 1, grid, threads, smem, stream, args...);
 }
 
 }  // namespace pa

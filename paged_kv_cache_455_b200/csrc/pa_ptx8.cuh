@@ -4,6 +4,8 @@
 
 #include <cstdint>
 
+#include <cuda_fp8.h>
+
 #include "pa_ptx.cuh"
 
 namespace pa {
@@ -98,6 +100,47 @@ __device__ __forceinline__ void tmem_hold(uint32_t (&r)[N])
         asm volatile("" : "+r"(r[i]));
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                     taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// Barrier of every (non-exited) thread of the cluster; orders their shared
+// and distributed shared memory accesses.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
+// The address of CTA `rank`'s copy of this CTA's shared-memory address.
+__device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 // Largest value of a warp (NaN ignored unless all are NaN).
 __device__ __forceinline__ float warp_max(float x)
 {
@@ -138,4 +181,14 @@ __device__ __forceinline__ bool barrier_or(int id, int threads, bool pred)
 }
 
 }  // namespace ptx
+
+// Two f16 values to E4M3 codes.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t x)
+{
+    __half2_raw h;
+    h.x = (unsigned short)(x & 0xffffu);
+    h.y = (unsigned short)(x >> 16);
+    return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
+}
+
 }  // namespace pa

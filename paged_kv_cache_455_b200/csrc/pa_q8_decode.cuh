@@ -281,15 +281,6 @@ __device__ __forceinline__ uint32_t e5m2x2(float lo, float hi)
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
 }
 
-// Two f16 values to E4M3 codes.
-__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t x)
-{
-    __half2_raw h;
-    h.x = (unsigned short)(x & 0xffffu);
-    h.y = (unsigned short)(x >> 16);
-    return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
-}
-
 template <int D, int G>
 __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
     q8_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,

@@ -19,7 +19,8 @@ pa_status run(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &t
                                            smem, &cap);
     if (st != PA_OK)
         return st;
-    return pa::launch_dependent(fn, grid, pa::kQpThreads, smem, stream, tq, tk, tv, p);
+    return pa::launch_clusters(fn, (unsigned)p.split, grid, pa::kQpThreads, smem, stream, tq, tk, tv,
+                               p);
 }
 
 template <int D>
@@ -86,7 +87,14 @@ extern "C" pa_status pa_prefill_attention_q8(void *out, const void *query,
     const int tq_tokens = pa::kQpRows / group;
     p.qblocks = (max_q_len + tq_tokens - 1) / tq_tokens;
     p.scale_log2 = scale * pa::kLog2e;
-    const int64_t grid = (int64_t)num_seqs * num_kv_heads * p.qblocks;
+    const int64_t blocks = (int64_t)num_seqs * num_kv_heads * p.qblocks;
+    // Clusters of up to eight CTAs per row block, as long as that makes at
+    // most four CTAs per SM and leaves each at least four tiles.
+    p.split = 1;
+    while (p.split < 8 && blocks * 2 * p.split <= 4 * 148 &&
+           max_context_len / pa::kQpTile >= 4 * 2 * p.split)
+        p.split *= 2;
+    const int64_t grid = blocks * p.split;
     if (grid > INT32_MAX)
         return PA_ERR_INVALID_ARG;
     alignas(64) CUtensorMap tq, tk, tv;

@@ -10,20 +10,31 @@
 // logits of each 16-token box by its block's K scale, and the weights by its
 // block's V scale before they are split: with m a running reference of
 // s + log2 vs,
-//     x = 2^5 vs 2^(s - m) = hi + lo,
-// hi the E4M3 part (x rounded to 4 bits; 0 below 2^-6), lo the rest as E5M2
-// (3 bits, down to 2^-16):  O += hi V + lo V.  A weight is off by 2^-7 of
-// itself at most (2^-3 below 2^-6), and by 2^-17 below E5M2's range, 2^-22 of
+//     x = 2^3 vs 2^(s - m) = hi + lo,
+// hi the E4M3 part (4 bits, down to 2^-6, subnormal to 2^-9), lo the rest as
+// E5M2 (3 bits, down to 2^-16):  O += hi V + lo V.  A weight is off by 2^-7 of
+// itself at most (2^-3 below 2^-6), and by 2^-17 below E5M2's range, 2^-20 of
 // the largest weight, so many small weights beside a large one are kept; row
 // sums take the fp32 weights.  The two products at twice bf16's rate cost as
 // much tensor time as one bf16 product would.
 //
-//   warps 0-3  softmax: one query row per thread
-//   warp 4     MMA issue, in the order S_{j+1}, P_{j-1} V_{j-1}
-//   warp 5     TMA of Q and K
-//   warp 6     TMA of V, block scales
+//   warps 0-7  softmax: warps w and w + 4 share 32 query rows, one per thread,
+//              and take half of a tile's columns each.  They move the rows'
+//              reference together, when either finds growth past 2^5 (a vote
+//              over both), and then rescale half of O each
+//   warp 8     MMA issue, in the order S_{j+1}, P_{j-1} V_{j-1}
+//   warp 9     TMA of Q and K
+//   warp 10    TMA of V, block scales
+// The softmax is what bounds it: exponentials and conversions, ~8 instructions
+// and 3 special-function ones per weight against the products' 1430 cycles a
+// tile; with four warps a tile took 4000 cycles.
 // Tensor memory columns: S [0, 64), O [64, 64 + d), Q hi and lo (d / 4 each,
 // four values per column), two weight buffers of 32 (hi 16, lo 16).
+//
+// Few query rows (drafted tokens, single chunks) over long contexts leave most
+// SMs idle, and there is no workspace to split into: then a cluster of SPLIT
+// CTAs shares a row block, each taking a part of the tiles, and joins the parts
+// through distributed shared memory.
 #pragma once
 
 #include "pa_prefill.cuh"
@@ -40,17 +51,17 @@ struct Q8PrefillParams {
     int total_q, num_q_heads, num_kv_heads;
     int max_blocks, block_size, bs_log2;
     int ctx_cap;
-    int qblocks;             // CTAs per (sequence, KV head)
+    int qblocks;             // row blocks per (sequence, KV head)
+    int split;               // CTAs (a cluster) per row block
     float scale_log2;
 };
 
 constexpr int kQpRows = 128;             // query rows per CTA
 constexpr int kQpTile = 64;              // tokens per stage
 constexpr int kQpBoxes = kQpTile / 16;
-constexpr int kQpThreads = 256;
-constexpr float kQpGrow = 3.f;           // log2 growth that makes a rescale
-constexpr float kQpWeight = 32.f;        // 2^5: a weight at the reference
-constexpr float kQpSplit = 0.015625f;    // 2^-6, E4M3's smallest normal
+constexpr int kQpThreads = 352;
+constexpr float kQpGrow = 5.f;           // log2 growth that makes a new reference
+constexpr float kQpWeight = 8.f;         // 2^3: a weight at the reference
 
 template <int D>
 struct Q8PrefillSmem {
@@ -62,13 +73,16 @@ struct Q8PrefillSmem {
     static constexpr int k_off = q_bytes;
     static constexpr int v_off = k_off + kStages * kStage;
     static constexpr int scale_off = v_off + kStages * kStage;   // [stage][ks 4, vs 4]
-    static constexpr int bar_off = scale_off + kStages * 2 * kQpBoxes * 4;
+    static constexpr int row_off = scale_off + kStages * 2 * kQpBoxes * 4;   // [2][rows] floats
+    static constexpr int bar_off = row_off + 2 * kQpRows * 4;
     // kfull, kempty, vfull, vempty [stages], pready[2], pfree[2], sfull, sfree, qfull, qready,
     // drain
     static constexpr int kBars = 4 * kStages + 9;
     static constexpr int flag_off = bar_off + 8 * kBars;
     static constexpr int bytes = 1024 + flag_off + 16;
     static_assert(bytes <= kSmemBudget, "shared memory per CTA");
+    // a split's accumulator, [row][D] fp32, goes where the stages were
+    static_assert(kQpRows * D * 4 <= 2 * kStages * kStage, "room for an accumulator");
     static constexpr uint32_t tmem_cols = 64 + D + D / 2 + 64 <= 256 ? 256u : 512u;
     static_assert(64 + D + D / 2 + 64 <= 512, "tensor memory columns");
 };
@@ -93,6 +107,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *gen = smem_raw + (base - raw);
     float *scales = reinterpret_cast<float *>(gen + L::scale_off);
+    float *rows_s = reinterpret_cast<float *>(gen + L::row_off);
     const uint32_t bars = base + L::bar_off;
     const uint32_t kfull = bars, kempty = kfull + 8 * S, vfull = kempty + 8 * S,
                    vempty = vfull + 8 * S, pready = vempty + 8 * S, pfree = pready + 16,
@@ -101,8 +116,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + L::flag_off);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen + L::flag_off + 4);
 
-    const int qb = blockIdx.x % p.qblocks;
-    const int rest = blockIdx.x / p.qblocks;
+    const int rank = blockIdx.x % p.split;               // within the cluster
+    const int qb = blockIdx.x / p.split % p.qblocks;
+    const int rest = blockIdx.x / p.split / p.qblocks;
     const int h = rest % p.num_kv_heads;
     const int b = rest / p.num_kv_heads;
 
@@ -120,9 +136,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         }
     };
     if (!rows_ok || n > ctx || ctx > p.ctx_cap) {
-        if (tid == 0 && qb == 0 && h == 0)
+        if (tid == 0 && qb == 0 && h == 0 && rank == 0)
             report(p.dev_status, PA_DEV_BAD_CONTEXT);
-        if (rows_ok && tok0 < n)
+        if (rows_ok && tok0 < n && rank == 0)
             zero_rows(min(TQ, n - tok0));
         return;
     }
@@ -130,22 +146,25 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         return;
     const int ntok = min(TQ, n - tok0);
     const int pos0 = ctx - n + tok0;
-    const int ntiles = (pos0 + ntok - 1) / kQpTile + 1;
-    const int last_tok = min(ntiles * kQpTile, ctx);     // tokens the tiles hold
+    const int all_tiles = (pos0 + ntok - 1) / kQpTile + 1;
+    const int last_tok = min(all_tiles * kQpTile, ctx);  // tokens the tiles hold
     const int nblk = (last_tok - 1) / p.block_size + 1;
-    auto boxes = [&](int j) { return min(kQpBoxes, (last_tok - j * kQpTile + 15) >> 4); };
+    // this CTA's tiles: first, first + 1, ...
+    const int first = (int)((int64_t)all_tiles * rank / p.split);
+    const int ntiles = (int)((int64_t)all_tiles * (rank + 1) / p.split) - first;
+    auto boxes = [&](int i) { return min(kQpBoxes, (last_tok - (first + i) * kQpTile + 15) >> 4); };
 
     if (tid == 0) {
         for (int i = 0; i < 4 * S; ++i)
             ptx::mbar_init(bars + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(pready + 8 * i, 4);
+            ptx::mbar_init(pready + 8 * i, 8);
             ptx::mbar_init(pfree + 8 * i, 1);
         }
         ptx::mbar_init(sfull, 1);
-        ptx::mbar_init(sfree, 4);
+        ptx::mbar_init(sfree, 8);
         ptx::mbar_init(qfull, 1);
-        ptx::mbar_init(qready, 4);
+        ptx::mbar_init(qready, 8);
         ptx::mbar_init(drain, 1);
         *abort_flag = 0;
     }
@@ -171,10 +190,12 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     if (bad) {
         if (tid == 0)
             report(p.dev_status, PA_DEV_BAD_BLOCK);
-    } else if (warp == 5 || warp == 6) {
+    } else if (ntiles == 0) {
+        // (a split of more CTAs than tiles)
+    } else if (warp == 9 || warp == 10) {
         // ================================================== TMA producers
         // lane x < 4 issues box x (tokens 16 x ..) of each tile
-        const bool is_k = warp == 5;
+        const bool is_k = warp == 9;
         const uint32_t full = is_k ? kfull : vfull, empty = is_k ? kempty : vempty;
         const void *tmap = is_k ? static_cast<const void *>(&tmap_k)
                                 : static_cast<const void *>(&tmap_v);
@@ -194,10 +215,11 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             const int i = bt * 32 + lane;
             return i < nblk ? __ldg(trow + i) : -1;
         };
-        int ids_cur = batch_ids(0), ids_next = batch_ids(1), cur_batch = 0;
+        int cur_batch = (first * kQpTile) >> (p.bs_log2 + 5);
+        int ids_cur = batch_ids(cur_batch), ids_next = batch_ids(cur_batch + 1);
         // this lane's box of tile i: its block, or -1 past the context
         auto box_id = [&](int i) {
-            const int blk = (i * kQpTile + (lane & 3) * 16) >> p.bs_log2;
+            const int blk = ((first + i) * kQpTile + (lane & 3) * 16) >> p.bs_log2;
             const int from_cur = __shfl_sync(kFull, ids_cur, blk & 31);
             const int from_next = __shfl_sync(kFull, ids_next, blk & 31);
             const int id = (blk >> 5) == cur_batch ? from_cur : from_next;
@@ -217,7 +239,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             if (__any_sync(kFull, *abort_flag != 0))
                 break;
             // the next tile's block and scales, a tile ahead of their use
-            const int bt = (i * kQpTile) >> (p.bs_log2 + 5);
+            const int bt = ((first + i) * kQpTile) >> (p.bs_log2 + 5);
             if (bt != cur_batch) {
                 cur_batch = bt;
                 ids_cur = ids_next;
@@ -241,7 +263,8 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 ptx::mbar_expect_tx(full + 8u * s, (uint32_t)(nbox * L::kBox));
             __syncwarp();
             if (lane < nbox) {
-                const int row = id * p.block_size + ((i * kQpTile + lane * 16) & (p.block_size - 1));
+                const int row = id * p.block_size +
+                                (((first + i) * kQpTile + lane * 16) & (p.block_size - 1));
                 ptx::tma_load_5d(dst + (uint32_t)(lane * L::kBox), tmap, 0, 0, 0, row >> 3, h,
                                  full + 8u * s, ptx::policy_evict_normal());
             }
@@ -269,7 +292,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 ptx::mbar_wait_bounded(full + 8u * (i % S), (uint32_t)((i / S) & 1), kWaitLimitNs);
         }
         __syncwarp();
-    } else if (warp == 4) {
+    } else if (warp == 8) {
         // ====================================================== MMA issue
         auto ready = [&](uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2) -> bool {
             if (__all_sync(kFull, ptx::mbar_test_wait(b1, p1) && ptx::mbar_test_wait(b2, p2)))
@@ -345,16 +368,34 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             ptx::mbar_wait_bounded(drain, 0, kWaitLimitNs);
         }
         __syncwarp();
-    } else if (warp < 4) {
+    } else {
         // =================================================== softmax warps
-        const int r = tid;                               // query row = TMEM lane
+        const int w4 = warp & 3, half = warp >> 2;       // columns 32 half .. of a tile
+        const int r = w4 * 32 + lane;                    // query row = TMEM lane
         const int pos = min(pos0 + r / G, ctx - 1);
-        const uint32_t lane_tm = (uint32_t)(warp * 32) << 16;
+        const uint32_t lane_tm = (uint32_t)(w4 * 32) << 16;
         float m_ref = -INFINITY, l = 0.f, fac = 0.f;
-        bool ok = __all_sync(kFull, ptx::mbar_wait_bounded(qfull, 0, kWaitLimitNs));
-        if (ok) {
+        bool fail = false;
+        auto give_up = [&]() {
+            fail = true;
+            if (lane == 0) {
+                report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
+                *abort_flag = 1;
+            }
+            __syncwarp();
+        };
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            if (fail || __all_sync(kFull, ptx::mbar_test_wait(bar, parity)))
+                return;
+            if (__any_sync(kFull, *abort_flag != 0) ||
+                !__all_sync(kFull, ptx::mbar_wait_bounded(bar, parity, kWaitLimitNs)))
+                give_up();
+        };
+        wait(qfull, 0);
+        if (!fail) {
             // this row of Q from its swizzled copy (64-element columns of
-            // 16384 bytes): the largest element first, then both parts
+            // 16384 bytes): its largest element, then both parts of this
+            // warp's half of the row
             auto unit = [&](int u8, uint32_t (&w)[4]) {     // elements 8 u8 .. 8 u8 + 7
                 const uint32_t a = base + (uint32_t)((u8 >> 3) * kQpRows * 128 + r * 128) +
                                    ((uint32_t)((u8 & 7) ^ (r & 7)) << 4);
@@ -378,7 +419,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             const float sigma = p.scale_log2 < 0.f ? -sig : sig;
             fac = ef < 255 ? p.scale_log2 / sigma : __int_as_float(0x7fc00000);
 #pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
+            for (int c = half * (D / 128); c < (half + 1) * (D / 128); ++c) {
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int v = 0; v < 8; ++v) {
@@ -409,26 +450,29 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             if (lane == 0)
                 ptx::mbar_arrive(qready);
         }
-        auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-            if (__all_sync(kFull, ptx::mbar_test_wait(bar, parity)))
-                return true;
-            if (__any_sync(kFull, *abort_flag != 0))
-                return false;
-            return __all_sync(kFull, ptx::mbar_wait_bounded(bar, parity, kWaitLimitNs));
-        };
-        for (int j = 0; ok && j < ntiles; ++j) {
-            const int s = j & 1, vsn = j % S;
-            if (!(ok = wait(sfull, (uint32_t)(j & 1))))
-                break;
-            ptx::tc_fence_after();
-            float sv[kQpTile];
-            {
-                uint32_t u0[16], u1[16], u2[16], u3[16];
-                const uint32_t sa = s_tm + lane_tm;
+        // Each iteration holds a barrier of both warps of the rows, also for a
+        // warp whose wait ran out; only what a barrier says ends the loop.
+        for (int i = 0; i < ntiles; ++i) {
+            const int s = i & 1, vsn = i % S;
+            wait(sfull, (uint32_t)(i & 1));
+            // V is in: so are the tile's block scales
+            wait(vfull + 8u * vsn, (uint32_t)((i / S) & 1));
+            float sv[32], kf[2], lv[2], vw[2], cand = -INFINITY;
+            const int tstart = (first + i) * kQpTile + 32 * half;
+            if (!fail) {
+                ptx::tc_fence_after();
+                uint32_t u0[16], u1[16];
+                const uint32_t sa = s_tm + lane_tm + (uint32_t)(32 * half);
                 ptx::tmem_ld16(sa, u0);
                 ptx::tmem_ld16(sa + 16, u1);
-                ptx::tmem_ld16(sa + 32, u2);
-                ptx::tmem_ld16(sa + 48, u3);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float f = fac * scales[vsn * 2 * kQpBoxes + 2 * half + x];
+                    const float v = scales[vsn * 2 * kQpBoxes + kQpBoxes + 2 * half + x];
+                    kf[x] = f == 0.f ? 1.2e-38f : f;     // (a masked -inf stays one)
+                    vw[x] = v * kQpWeight;
+                    lv[x] = fmaxf(ptx::lg2(v), -64.f);
+                }
                 ptx::tmem_wait_ld();
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -436,156 +480,163 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     ptx::mbar_arrive(sfree);
                 ptx::tmem_hold16(u0);
                 ptx::tmem_hold16(u1);
-                ptx::tmem_hold16(u2);
-                ptx::tmem_hold16(u3);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     sv[e] = __uint_as_float(u0[e]);
                     sv[16 + e] = __uint_as_float(u1[e]);
-                    sv[32 + e] = __uint_as_float(u2[e]);
-                    sv[48 + e] = __uint_as_float(u3[e]);
+                }
+                if (tstart + 31 > pos0) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        sv[c] = tstart + c <= pos ? sv[c] : -INFINITY;
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float a = sv[16 * x], c = sv[16 * x + 1];
+#pragma unroll
+                    for (int e = 2; e < 16; e += 2) {
+                        a = fmaxf(a, sv[16 * x + e]);
+                        c = fmaxf(c, sv[16 * x + e + 1]);
+                    }
+                    cand = fmaxf(cand, fmaf(fmaxf(a, c), kf[x], lv[x]));
                 }
             }
-            // V_j is in: so are the tile's block scales
-            if (!(ok = wait(vfull + 8u * vsn, (uint32_t)((j / S) & 1))))
-                break;
-            float kf[kQpBoxes], vw[kQpBoxes], lv[kQpBoxes];
-#pragma unroll
-            for (int x = 0; x < kQpBoxes; ++x) {
-                const float f = fac * scales[vsn * 2 * kQpBoxes + x];
-                const float v = scales[vsn * 2 * kQpBoxes + kQpBoxes + x];
-                kf[x] = f == 0.f ? 1.2e-38f : f;         // (a masked -inf stays one)
-                vw[x] = v * kQpWeight;
-                lv[x] = fmaxf(ptx::lg2(v), -64.f);
-            }
-            const int tstart = j * kQpTile;
-            if (tstart + kQpTile - 1 > pos0) {
-#pragma unroll
-                for (int c = 0; c < kQpTile; ++c)
-                    sv[c] = tstart + c <= pos ? sv[c] : -INFINITY;
-            }
-            float mx = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < kQpBoxes; ++x) {
-                float a = sv[16 * x], c = sv[16 * x + 1];
-#pragma unroll
-                for (int e = 2; e < 16; e += 2) {
-                    a = fmaxf(a, sv[16 * x + e]);
-                    c = fmaxf(c, sv[16 * x + e + 1]);
-                }
-                mx = fmaxf(mx, fmaf(fmaxf(a, c), kf[x], lv[x]));
-            }
-            bool grow = false;
-            float alpha = 1.f;
-            if (m_ref == -INFINITY) {
-                m_ref = mx;
-            } else if (mx > m_ref + kQpGrow) {
-                grow = true;
-                alpha = ptx::ex2(m_ref - mx);
-            }
-            if (__any_sync(kFull, grow)) {
-                // P_{j-1} V_{j-1} (and all before) must be in O
-                if (!(ok = wait(pfree + 8u * (s ^ 1), (uint32_t)(((j - 1) >> 1) & 1))))
+            if (ptx::barrier_or(1 + w4, 64, cand > m_ref + kQpGrow || fail)) {
+                rows_s[half * kQpRows + r] = cand;
+                if (ptx::barrier_or(5 + w4, 64, fail)) {
+                    fail = true;
                     break;
-                ptx::tc_fence_after();
+                }
+                const float mx = fmaxf(cand, rows_s[(half ^ 1) * kQpRows + r]);
+                float alpha = 1.f;
+                if (mx > m_ref + kQpGrow) {
+                    if (m_ref != -INFINITY)
+                        alpha = ptx::ex2(m_ref - mx);    // (else nothing to rescale)
+                    l *= alpha;
+                    m_ref = mx;
+                }
+                if (__any_sync(kFull, alpha != 1.f)) {
+                    // P V of the tile before (and all earlier) must be in O
+                    wait(pfree + 8u * (s ^ 1), (uint32_t)(((i - 1) >> 1) & 1));
+                    ptx::tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
+                    for (int c = half * (D / 32); c < (half + 1) * (D / 32) && !fail; ++c) {
+                        uint32_t u[16];
+                        ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 16), u);
+                        ptx::tmem_wait_ld();
+                        ptx::tmem_hold16(u);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+                        ptx::tmem_st16(o_tm + lane_tm + (uint32_t)(c * 16), u);
+                    }
+                    ptx::tmem_wait_st();
+                }
+            }
+            if (i >= 2)
+                wait(pfree + 8u * s, (uint32_t)(((i - 2) >> 1) & 1));
+            if (!fail) {
+                ptx::tc_fence_after();
+                const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
+                uint32_t hi[8], lo[8];
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int x = k >> 2;
+                    uint32_t h2[2], r2[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float e0 = ptx::ex2(fmaf(sv[4 * k + 2 * e], kf[x], nref));
+                        const float e1 = ptx::ex2(fmaf(sv[4 * k + 2 * e + 1], kf[x], nref));
+                        l4[2 * (k & 1) + e] += e0 + e1;
+                        // (11 bits and 2^-24: far below what hi + lo keep)
+                        const uint32_t y = ptx::pack_f16x2(e0 * vw[x], e1 * vw[x]);
+                        h2[e] = f16x2_to_e4m3x2(y);
+                        // the rest as E5M2, the upper byte of an f16: rounded
+                        // (half away from zero) by an add below it
+                        r2[e] = ptx::sub_f16x2(y, e4m3x2_to_f16x2(h2[e])) + 0x00800080u;
+                    }
+                    hi[k] = h2[0] | (h2[1] << 16);
+                    lo[k] = ptx::prmt(r2[0], r2[1], 0x7531u);
+                }
+                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                ptx::tmem_st8(p_tm + lane_tm + (uint32_t)(s * 32 + 8 * half), hi);
+                ptx::tmem_st8(p_tm + lane_tm + (uint32_t)(s * 32 + 16 + 8 * half), lo);
+                const int from = last_tok - tstart;      // tokens of this half
+                if (from > 0 && from < 32) {
+                    // V rows of a 32-token step past the context: their weight
+                    // is 0, but 0 * NaN is NaN (the half's four warps together)
+                    const uint32_t vst = base + (uint32_t)(L::v_off + vsn * L::kStage);
+                    for (int idx = r; idx < (32 - from) * NCH * 8; idx += kQpRows) {
+                        const int t = 32 * half + from + idx / (NCH * 8), c = idx % (NCH * 8);
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         vst + (uint32_t)((t >> 3) * L::kGroup + (c >> 3) * 1024 +
+                                                          (t & 7) * 128 + (c & 7) * 16)),
+                                     "r"(0)
+                                     : "memory");
+                    }
+                    ptx::fence_proxy_async_smem();
+                }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(pready + 8u * s);
+            }
+        }
+        wait(pfree + 8u * ((ntiles - 1) & 1), (uint32_t)(((ntiles - 1) >> 1) & 1));
+        // both halves' sums; with a split, the row's reference and sum for the
+        // other CTAs (a warp that gave up takes part in the barriers too)
+        ptx::barrier_or(1 + w4, 64, false);              // (rows_s has been read)
+        rows_s[half * kQpRows + r] = l;
+        ptx::barrier_or(1 + w4, 64, false);
+        l += rows_s[(half ^ 1) * kQpRows + r];
+        ptx::barrier_or(1 + w4, 64, false);
+        if (half == 0) {
+            rows_s[r] = m_ref;
+            rows_s[kQpRows + r] = l;
+        }
+        if (!fail) {
+            ptx::tc_fence_after();
+            if (p.split == 1) {
+                // (a sum that is not a number, from a non-finite query, stays one)
+                const float inv = l == 0.f ? 0.f : __frcp_rn(l) * (1.f / kQpWeight);
+                const bool store = r / G < ntok;
+                uint4 *dst = reinterpret_cast<uint4 *>(
+                    p.out +
+                    ((int64_t)(q0 + tok0 + (store ? r / G : 0)) * p.num_q_heads + h * G + r % G) * D);
+#pragma unroll 1
+                for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
+                    uint32_t u[16], o[8];
+                    ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 16), u);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_hold16(u);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        o[k] = ptx::pack_bf16x2(__uint_as_float(u[2 * k]) * inv,
+                                                __uint_as_float(u[2 * k + 1]) * inv);
+                    if (store) {
+                        dst[2 * c] = make_uint4(o[0], o[1], o[2], o[3]);
+                        dst[2 * c + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+            } else {
+                // the accumulator to shared memory, where the stages were
+                // (16-byte unit u of row r at u ^ (r & 31))
+#pragma unroll 1
+                for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
                     uint32_t u[16];
                     ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 16), u);
                     ptx::tmem_wait_ld();
                     ptx::tmem_hold16(u);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-                    ptx::tmem_st16(o_tm + lane_tm + (uint32_t)(c * 16), u);
-                }
-                ptx::tmem_wait_st();
-            }
-            if (grow) {
-                l *= alpha;
-                m_ref = mx;
-            }
-            const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
-            uint32_t hi[16], lo[16];
-            float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const int x = k >> 2;
-                float e[4], a[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    e[i] = ptx::ex2(fmaf(sv[4 * k + i], kf[x], nref));
-                    l4[i] += e[i];
-                    e[i] *= vw[x];
-                    // 4 bits, to nearest; nothing below E4M3's normals
-                    a[i] = e[i] < kQpSplit
-                               ? 0.f
-                               : __uint_as_float((__float_as_uint(e[i]) + 0x80000u) & 0xfff00000u);
-                }
-                hi[k] = f32x2_to_e4m3x2(a[0], a[1]) | (f32x2_to_e4m3x2(a[2], a[3]) << 16);
-                lo[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(e[0] - a[0], e[1] - a[1]),
-                                                           __NV_SATFINITE, __NV_E5M2) |
-                        ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(e[2] - a[2], e[3] - a[3]),
-                                                            __NV_SATFINITE, __NV_E5M2)
-                         << 16);
-            }
-            l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-            if (j >= 2) {
-                if (!(ok = wait(pfree + 8u * s, (uint32_t)(((j - 2) >> 1) & 1))))
-                    break;
-                ptx::tc_fence_after();
-            }
-            ptx::tmem_st16(p_tm + lane_tm + (uint32_t)(s * 32), hi);
-            ptx::tmem_st16(p_tm + lane_tm + (uint32_t)(s * 32 + 16), lo);
-            if (tstart + kQpTile > last_tok && ((last_tok - tstart) & 31) != 0) {
-                // V rows of the last 32-token step past the context: their
-                // weight is 0, but 0 * NaN is NaN
-                const int from = last_tok - tstart, to = (from + 31) & ~31;
-                const uint32_t vst = base + (uint32_t)(L::v_off + vsn * L::kStage);
-                for (int idx = r; idx < (to - from) * NCH * 8; idx += kQpRows) {
-                    const int t = from + idx / (NCH * 8), c = idx % (NCH * 8);
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                     vst + (uint32_t)((t >> 3) * L::kGroup + (c >> 3) * 1024 +
-                                                      (t & 7) * 128 + (c & 7) * 16)),
-                                 "r"(0)
-                                 : "memory");
-                }
-                ptx::fence_proxy_async_smem();
-            }
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                ptx::mbar_arrive(pready + 8u * s);
-        }
-        if (ok && !wait(pfree + 8u * ((ntiles - 1) & 1), (uint32_t)(((ntiles - 1) >> 1) & 1)))
-            ok = false;
-        if (!ok) {
-            if (lane == 0) {
-                report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
-                *abort_flag = 1;
-            }
-            __syncwarp();
-        } else {
-            ptx::tc_fence_after();
-            // (a sum that is not a number, from a non-finite query, stays one)
-            const float inv = l == 0.f ? 0.f : __frcp_rn(l) * (1.f / kQpWeight);
-            const bool store = r / G < ntok;
-            uint4 *dst = reinterpret_cast<uint4 *>(
-                p.out + ((int64_t)(q0 + tok0 + (store ? r / G : 0)) * p.num_q_heads + h * G + r % G) * D);
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-                uint32_t u[16], o[8];
-                ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 16), u);
-                ptx::tmem_wait_ld();
-                ptx::tmem_hold16(u);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    o[k] = ptx::pack_bf16x2(__uint_as_float(u[2 * k]) * inv,
-                                            __uint_as_float(u[2 * k + 1]) * inv);
-                if (store) {
-                    dst[2 * c] = make_uint4(o[0], o[1], o[2], o[3]);
-                    dst[2 * c + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+                    for (int k = 0; k < 4; ++k)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         base + (uint32_t)(L::k_off + r * D * 4) +
+                                         ((uint32_t)((4 * c + k) ^ (r & 31)) << 4)),
+                                     "r"(u[4 * k]), "r"(u[4 * k + 1]), "r"(u[4 * k + 2]),
+                                     "r"(u[4 * k + 3])
+                                     : "memory");
                 }
             }
         }
@@ -593,11 +644,58 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    // zeros for an invalid block and for a wait that ran out
-    if (bad || *abort_flag != 0)
-        zero_rows(ntok);
     if (warp == 0)
         ptx::tmem_dealloc(tmem, L::tmem_cols);
+    if (p.split == 1) {
+        // zeros for an invalid block and for a wait that ran out
+        if (bad || *abort_flag != 0)
+            zero_rows(ntok);
+        return;
+    }
+    // ---- join the cluster's parts: row r by CTA r % split, a warp per row
+    if (ntiles == 0 && tid < kQpRows) {
+        rows_s[tid] = -INFINITY;
+        rows_s[kQpRows + tid] = 0.f;
+    }
+    ptx::cluster_sync();
+    const uint32_t rows_a = base + L::row_off, acc_a = base + L::k_off, flag_a = base + L::flag_off;
+    bool lost = bad;
+    for (int c = 0; c < p.split; ++c)
+        lost |= ptx::ld_cluster_f32(ptx::map_cluster(flag_a, c)) != 0.f;
+    for (int r = rank + p.split * warp; r < ntok * G; r += p.split * (kQpThreads / 32)) {
+        float M = -INFINITY, sum = 0.f;
+        for (int c = 0; c < p.split; ++c)
+            M = fmaxf(M, ptx::ld_cluster_f32(ptx::map_cluster(rows_a + 4 * r, c)));
+        float4 a[D / 128];
+#pragma unroll
+        for (int k = 0; k < D / 128; ++k)
+            a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < p.split && !lost; ++c) {
+            const float m = ptx::ld_cluster_f32(ptx::map_cluster(rows_a + 4 * r, c));
+            const float ls = ptx::ld_cluster_f32(ptx::map_cluster(rows_a + 4 * (kQpRows + r), c));
+            if (m == -INFINITY && ls == 0.f)
+                continue;                                // no token of this part is seen
+            const float f = ptx::ex2(m - M);
+            sum += ls * f;
+            const uint32_t row = ptx::map_cluster(acc_a + (uint32_t)(r * D * 4), c);
+#pragma unroll
+            for (int k = 0; k < D / 128; ++k) {
+                const float4 v =
+                    ptx::ld_cluster_f32x4(row + ((uint32_t)((lane + 32 * k) ^ (r & 31)) << 4));
+                a[k].x = fmaf(v.x, f, a[k].x);
+                a[k].y = fmaf(v.y, f, a[k].y);
+                a[k].z = fmaf(v.z, f, a[k].z);
+                a[k].w = fmaf(v.w, f, a[k].w);
+            }
+        }
+        const float inv = sum == 0.f ? 0.f : __frcp_rn(sum) * (1.f / kQpWeight);
+        __nv_bfloat16 *dst =
+            p.out + ((int64_t)(q0 + tok0 + r / G) * p.num_q_heads + h * G + r % G) * D + 4 * lane;
+#pragma unroll
+        for (int k = 0; k < D / 128; ++k)
+            store4(dst + 128 * k, make_float4(a[k].x * inv, a[k].y * inv, a[k].z * inv, a[k].w * inv));
+    }
+    ptx::cluster_sync();                                 // the others may still be reading
 }
 
 }  // namespace pa

@@ -9,9 +9,12 @@ logits s_t and values V_t (everything else is fp32 or exact):
             element is off by at most 2^-10, that is 2^-17 of the row's
             largest, and s_t by d_t = |scale| 2^-17 max|q| sum_i |K_ti|.
             Numerator and sum move by at most that share: 2 max_t d_t in all.
-  weights   decode: three E5M2 parts of 3 bits, half a step each: 2^-9.
-            prefill: a 4-bit part and a 3-bit one: 2^-7; weights below 2^-11 of
-            the largest p_t vs_t may have the 3-bit part alone: 2^-3.
+  weights   x_t = p_t vs_t, scaled.  Decode: three E5M2 parts of 3 bits, half a
+            step each, 2^-9 of x_t, or half the quantum 2^-16 of the last part,
+            which counts 2^-6: 2^-23, where the largest x_t is at least 1.
+            Prefill: hi of 4 bits (half a step 2^-4, or half the quantum 2^-9),
+            lo the rest with 3 bits (half a step 2^-3): 2^-7 of x_t or 2^-13,
+            where the largest x_t is at least 2^3, that is 2^-16 of it.
   output    bf16, half a step: 2^-8 of it.
 
 fp32 accumulation and the exponential add less than 2^-12 of sum p |V|.
@@ -51,12 +54,9 @@ def attention_with_bound(q, kp, vp, ks, vs, tab, lens, cu, scale, prefill):
             dt = abs(scale) * 2.0 ** -17 * np.abs(rows).max(axis=1)[:, None] * \
                 np.abs(K[:, g]).sum(axis=1)[None, :]
             shift = 2 * np.where(seen, dt, 0).max(axis=1, keepdims=True)
-            if prefill:
-                pv = p * sc[None, :, g]
-                share = np.where(pv < 2.0 ** -11 * pv.max(axis=1, keepdims=True), 2.0 ** -3,
-                                 2.0 ** -7)
-            else:
-                share = 2.0 ** -9
-            w = p * (share + shift + EXTRA)
+            x = p * sc[None, :, g]
+            rel, least = (2.0 ** -7, 2.0 ** -16) if prefill else (2.0 ** -9, 2.0 ** -23)
+            off = least * x.max(axis=1, keepdims=True) / sc[None, :, g]
+            w = p * (rel + shift + EXTRA) + np.where(seen, off, 0)
             tol[q0:q0 + n, h] = w @ np.abs(V[:, g])
     return ref, tol + 2.0 ** -8 * np.abs(ref)

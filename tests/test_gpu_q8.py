@@ -307,3 +307,21 @@ def test_decode_wait_that_runs_out(pa, cta):
     for b in range(12):
         assert (out[b] == 0).all() if b in lost else torch.equal(out[b], want[b])
     assert torch.equal(c.decode(pa, ws=ws), want)
+
+
+@pytest.mark.parametrize("lens,chunks,hq,hkv,d,bs", [
+    ([4000], [5], 4, 1, 256, 16),                       # clusters of eight
+    ([3000, 40, 900, 2111], [5, 5, 1, 17], 16, 4, 256, 16),
+    ([70] * 20 + [2600], [3] * 21, 8, 1, 128, 32),      # parts without a tile
+    ([1500, 1400], [200, 33], 16, 2, 128, 16),
+])
+def test_prefill_of_few_rows_over_long_contexts(pa, lens, chunks, hq, hkv, d, bs):
+    c = Case(sum(lens) + d, lens, hq, hkv, d, bs, chunks=chunks)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = c.prefill(pa, status)
+    assert int(status.item()) == 0
+    c.check(out, True)
+    c.tab[0, -1 if len(lens) == 1 else 0] = -1
+    out = c.prefill(pa, status)
+    assert int(status.item()) == pa.PA_DEV_BAD_BLOCK
+    assert (out[:c.cu[1]] == 0).all() and torch.isfinite(out).all()
