@@ -10,26 +10,26 @@
 // logits of each 16-token box by its block's K scale, and the weights by its
 // block's V scale before they are split: with m a running reference of
 // s + log2 vs,
-//     x = 2^3 vs 2^(s - m) = hi + lo,
+//     x = vs 2^(s - m) = hi + lo,
 // hi the E4M3 part (4 bits, down to 2^-6, subnormal to 2^-9), lo the rest as
 // E5M2 (3 bits, down to 2^-16):  O += hi V + lo V.  A weight is off by 2^-7 of
-// itself at most (2^-3 below 2^-6), and by 2^-17 below E5M2's range, 2^-20 of
-// the largest weight, so many small weights beside a large one are kept; row
-// sums take the fp32 weights.  The two products at twice bf16's rate cost as
-// much tensor time as one bf16 product would.
+// itself or 2^-13, where the largest weight is at least 1 (m moves only once a
+// weight would pass 2^8); row sums take the fp32 weights.  The two products at
+// twice bf16's rate cost as much tensor time as one bf16 product would.
 //
-//   warps 0-7  softmax: warps w and w + 4 share 32 query rows, one per thread,
-//              and take half of a tile's columns each.  They move the rows'
-//              reference together, when either finds growth past 2^5 (a vote
-//              over both), and then rescale half of O each
-//   warp 8     MMA issue, in the order S_{j+1}, P_{j-1} V_{j-1}
+//   warps 0-7  softmax: two sets of four warps take alternate tiles, one query
+//              row per thread.  A set settles the rows' reference for its tile
+//              and passes it on to the other set before it goes on to the
+//              exponentials, so one set's exponentials run beside the other's
+//              loads, maximum and waits
+//   warp 8     MMA issue: P_j V_j, then S_{j+2}
 //   warp 9     TMA of Q and K
 //   warp 10    TMA of V, block scales
-// The softmax is what bounds it: exponentials and conversions, ~8 instructions
-// and 3 special-function ones per weight against the products' 1430 cycles a
-// tile; with four warps a tile took 4000 cycles.
-// Tensor memory columns: S [0, 64), O [64, 64 + d), Q hi and lo (d / 4 each,
-// four values per column), two weight buffers of 32 (hi 16, lo 16).
+// Tensor memory columns: S buffers of 64 at 0 and 64, O [128, 128 + d), Q hi
+// and lo (d / 4 each, four values per column).  The weights of tile j (hi 16
+// columns, lo 16) take the place of S_j once its rows have been read.
+// The special-function unit bounds it: two exponentials and two conversions
+// per pair of weights are ~1024 cycles a tile, the products 1050.  MEASURE
 //
 // Few query rows (drafted tokens, single chunks) over long contexts leave most
 // SMs idle, and there is no workspace to split into: then a cluster of SPLIT
@@ -60,8 +60,7 @@ constexpr int kQpRows = 128;             // query rows per CTA
 constexpr int kQpTile = 64;              // tokens per stage
 constexpr int kQpBoxes = kQpTile / 16;
 constexpr int kQpThreads = 352;
-constexpr float kQpGrow = 5.f;           // log2 growth that makes a new reference
-constexpr float kQpWeight = 8.f;         // 2^3: a weight at the reference
+constexpr float kQpGrow = 8.f;           // log2 growth that makes a new reference
 
 template <int D>
 struct Q8PrefillSmem {
@@ -75,16 +74,16 @@ struct Q8PrefillSmem {
     static constexpr int scale_off = v_off + kStages * kStage;   // [stage][ks 4, vs 4]
     static constexpr int row_off = scale_off + kStages * 2 * kQpBoxes * 4;   // [2][rows] floats
     static constexpr int bar_off = row_off + 2 * kQpRows * 4;
-    // kfull, kempty, vfull, vempty [stages], pready[2], pfree[2], sfull, sfree, qfull, qready,
-    // drain
-    static constexpr int kBars = 4 * kStages + 9;
+    // kfull, kempty, vfull, vempty [stages], pready[2], pvdone[2], sfull[2], qfull, qready,
+    // drain, settled[2][4]
+    static constexpr int kBars = 4 * kStages + 17;
     static constexpr int flag_off = bar_off + 8 * kBars;
     static constexpr int bytes = 1024 + flag_off + 16;
     static_assert(bytes <= kSmemBudget, "shared memory per CTA");
     // a split's accumulator, [row][D] fp32, goes where the stages were
     static_assert(kQpRows * D * 4 <= 2 * kStages * kStage, "room for an accumulator");
-    static constexpr uint32_t tmem_cols = 64 + D + D / 2 + 64 <= 256 ? 256u : 512u;
-    static_assert(64 + D + D / 2 + 64 <= 512, "tensor memory columns");
+    static constexpr uint32_t tmem_cols = 512;
+    static_assert(128 + D + D / 2 <= 512, "tensor memory columns");
 };
 
 template <int D, int G>
@@ -110,9 +109,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     float *rows_s = reinterpret_cast<float *>(gen + L::row_off);
     const uint32_t bars = base + L::bar_off;
     const uint32_t kfull = bars, kempty = kfull + 8 * S, vfull = kempty + 8 * S,
-                   vempty = vfull + 8 * S, pready = vempty + 8 * S, pfree = pready + 16,
-                   sfull = pfree + 16, sfree = sfull + 8, qfull = sfree + 8, qready = qfull + 8,
-                   drain = qready + 8;
+                   vempty = vfull + 8 * S, pready = vempty + 8 * S, pvdone = pready + 16,
+                   sfull = pvdone + 16, qfull = sfull + 16, qready = qfull + 8, drain = qready + 8,
+                   settled = drain + 8;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + L::flag_off);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen + L::flag_off + 4);
 
@@ -158,11 +157,12 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         for (int i = 0; i < 4 * S; ++i)
             ptx::mbar_init(bars + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(pready + 8 * i, 8);
-            ptx::mbar_init(pfree + 8 * i, 1);
+            ptx::mbar_init(pready + 8 * i, 4);
+            ptx::mbar_init(pvdone + 8 * i, 1);
+            ptx::mbar_init(sfull + 8 * i, 1);
         }
-        ptx::mbar_init(sfull, 1);
-        ptx::mbar_init(sfree, 8);
+        for (int i = 0; i < 8; ++i)
+            ptx::mbar_init(settled + 8 * i, 1);
         ptx::mbar_init(qfull, 1);
         ptx::mbar_init(qready, 8);
         ptx::mbar_init(drain, 1);
@@ -183,9 +183,8 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     bad = __syncthreads_or(bad);
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    const uint32_t s_tm = tmem, o_tm = tmem + 64;
+    const uint32_t s_tm = tmem, o_tm = tmem + 128;
     const uint32_t qh_tm = o_tm + D, ql_tm = qh_tm + D / 4;
-    const uint32_t p_tm = ql_tm + D / 4;          // buffer s at + 32 s: hi 16 columns, lo 16
 
     if (bad) {
         if (tid == 0)
@@ -304,6 +303,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         };
         auto issue_s = [&](int j) {
             ptx::tc_fence_after();
+            const uint32_t d = s_tm + (uint32_t)((j & 1) * 64);
             const uint64_t kd = ptx::umma_desc_sw128(
                 base + (uint32_t)(L::k_off + (j % S) * L::kStage), 16, L::kGroup);
             if (ptx::elect_one()) {
@@ -311,10 +311,10 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 for (int kk = 0; kk < D / 32; ++kk) {
                     const uint64_t at =
                         kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
-                    ptx::umma_f8_ts(s_tm, qh_tm + (uint32_t)(kk * 8), at, IDESC_S, kk > 0);
-                    ptx::umma_f8_ts(s_tm, ql_tm + (uint32_t)(kk * 8), at, IDESC_S, true);
+                    ptx::umma_f8_ts(d, qh_tm + (uint32_t)(kk * 8), at, IDESC_S, kk > 0);
+                    ptx::umma_f8_ts(d, ql_tm + (uint32_t)(kk * 8), at, IDESC_S, true);
                 }
-                ptx::umma_commit(sfull);
+                ptx::umma_commit(sfull + 8u * (j & 1));
                 ptx::umma_commit(kempty + 8u * (j % S));
             }
             __syncwarp();
@@ -331,12 +331,12 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             if (ptx::elect_one()) {
                 for (int t = 0; t < steps; ++t) {
                     const uint64_t at = vd + (uint64_t)((t * 2 * L::kBox) >> 4);
-                    const uint32_t pa0 = p_tm + (uint32_t)(s * 32 + t * 8);
+                    const uint32_t pa0 = s_tm + (uint32_t)(s * 64 + t * 8);
                     ptx::umma_f8_ts(o_tm, pa0, at, IDESC_HI, j > 0 || t > 0);
                     ptx::umma_f8_ts(o_tm, pa0 + 16, at, IDESC_LO, true);
                 }
+                ptx::umma_commit(pvdone + 8u * s);
                 ptx::umma_commit(vempty + 8u * vsn);
-                ptx::umma_commit(pfree + 8u * s);
             }
             __syncwarp();
             return true;
@@ -344,18 +344,19 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         bool ok = ready(qready, 0, kfull, 0);
         if (ok)
             issue_s(0);
+        if (ok && ntiles > 1 && (ok = ready(kfull + 8u * (1 % S), 0, qready, 0)))
+            issue_s(1);
         for (int j = 0; ok && j < ntiles; ++j) {
-            if (j + 1 < ntiles) {
-                if (!(ok = ready(sfree, (uint32_t)(j & 1), kfull + 8u * ((j + 1) % S),
-                                 (uint32_t)(((j + 1) / S) & 1))))
-                    break;
-                issue_s(j + 1);
-            }
-            if (j >= 1 && !(ok = issue_pv(j - 1)))
+            if (!(ok = issue_pv(j)))
                 break;
+            // S_{j+2} goes where the weights of tile j were
+            if (j + 2 < ntiles) {
+                if (!(ok = ready(kfull + 8u * ((j + 2) % S), (uint32_t)(((j + 2) / S) & 1),
+                                 pvdone + 8u * (j & 1), (uint32_t)((j >> 1) & 1))))
+                    break;
+                issue_s(j + 2);
+            }
         }
-        if (ok)
-            ok = issue_pv(ntiles - 1);
         if (!ok) {
             if (lane == 0) {
                 report(p.dev_status, PA_DEV_WAIT_TIMEOUT);
@@ -370,11 +371,11 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         __syncwarp();
     } else {
         // =================================================== softmax warps
-        const int w4 = warp & 3, half = warp >> 2;       // columns 32 half .. of a tile
+        const int w4 = warp & 3, half = warp >> 2;       // tiles half, half + 2, ...
         const int r = w4 * 32 + lane;                    // query row = TMEM lane
         const int pos = min(pos0 + r / G, ctx - 1);
         const uint32_t lane_tm = (uint32_t)(w4 * 32) << 16;
-        float m_ref = -INFINITY, l = 0.f, fac = 0.f;
+        float m_ref = -INFINITY, l = 0.f, fac = 0.f;     // l relative to m_ref
         bool fail = false;
         auto give_up = [&]() {
             fail = true;
@@ -450,104 +451,112 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             if (lane == 0)
                 ptx::mbar_arrive(qready);
         }
-        // Each iteration holds a barrier of both warps of the rows, also for a
-        // warp whose wait ran out; only what a barrier says ends the loop.
-        for (int i = 0; i < ntiles; ++i) {
+        // the reference that the other set's warp of these rows left with tile
+        // i (and with it this warp's sum in the same terms)
+        auto take_reference = [&](int i) {
+            wait(settled + 8u * (4 * (i & 1) + w4), (uint32_t)((i >> 1) & 1));
+            const float m = rows_s[r];
+            if (m != m_ref && m_ref != -INFINITY)
+                l *= ptx::ex2(m_ref - m);
+            m_ref = m;
+        };
+        for (int i = half; i < ntiles && !fail; i += 2) {
             const int s = i & 1, vsn = i % S;
-            wait(sfull, (uint32_t)(i & 1));
+            wait(sfull + 8u * s, (uint32_t)((i >> 1) & 1));
             // V is in: so are the tile's block scales
             wait(vfull + 8u * vsn, (uint32_t)((i / S) & 1));
-            float sv[32], kf[2], lv[2], vw[2], cand = -INFINITY;
-            const int tstart = (first + i) * kQpTile + 32 * half;
-            if (!fail) {
-                ptx::tc_fence_after();
-                uint32_t u0[16], u1[16];
-                const uint32_t sa = s_tm + lane_tm + (uint32_t)(32 * half);
+            if (fail)
+                break;
+            ptx::tc_fence_after();
+            const int tstart = (first + i) * kQpTile;
+            const uint32_t sa = s_tm + lane_tm + (uint32_t)(s * 64);
+            float sv[kQpTile], kf[kQpBoxes], lv[kQpBoxes], vw[kQpBoxes], cand = -INFINITY;
+            {
+                uint32_t u0[16], u1[16], u2[16], u3[16];
                 ptx::tmem_ld16(sa, u0);
                 ptx::tmem_ld16(sa + 16, u1);
+                ptx::tmem_ld16(sa + 32, u2);
+                ptx::tmem_ld16(sa + 48, u3);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float f = fac * scales[vsn * 2 * kQpBoxes + 2 * half + x];
-                    const float v = scales[vsn * 2 * kQpBoxes + kQpBoxes + 2 * half + x];
+                for (int x = 0; x < kQpBoxes; ++x) {
+                    const float f = fac * scales[vsn * 2 * kQpBoxes + x];
+                    vw[x] = scales[vsn * 2 * kQpBoxes + kQpBoxes + x];
                     kf[x] = f == 0.f ? 1.2e-38f : f;     // (a masked -inf stays one)
-                    vw[x] = v * kQpWeight;
-                    lv[x] = fmaxf(ptx::lg2(v), -64.f);
+                    lv[x] = fmaxf(ptx::lg2(vw[x]), -64.f);
                 }
                 ptx::tmem_wait_ld();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    ptx::mbar_arrive(sfree);
                 ptx::tmem_hold16(u0);
                 ptx::tmem_hold16(u1);
+                ptx::tmem_hold16(u2);
+                ptx::tmem_hold16(u3);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     sv[e] = __uint_as_float(u0[e]);
                     sv[16 + e] = __uint_as_float(u1[e]);
-                }
-                if (tstart + 31 > pos0) {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        sv[c] = tstart + c <= pos ? sv[c] : -INFINITY;
-                }
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float a = sv[16 * x], c = sv[16 * x + 1];
-#pragma unroll
-                    for (int e = 2; e < 16; e += 2) {
-                        a = fmaxf(a, sv[16 * x + e]);
-                        c = fmaxf(c, sv[16 * x + e + 1]);
-                    }
-                    cand = fmaxf(cand, fmaf(fmaxf(a, c), kf[x], lv[x]));
+                    sv[32 + e] = __uint_as_float(u2[e]);
+                    sv[48 + e] = __uint_as_float(u3[e]);
                 }
             }
-            if (ptx::barrier_or(1 + w4, 64, cand > m_ref + kQpGrow || fail)) {
-                rows_s[half * kQpRows + r] = cand;
-                if (ptx::barrier_or(5 + w4, 64, fail)) {
-                    fail = true;
+            if (tstart + kQpTile - 1 > pos0) {
+#pragma unroll
+                for (int c = 0; c < kQpTile; ++c)
+                    sv[c] = tstart + c <= pos ? sv[c] : -INFINITY;
+            }
+#pragma unroll
+            for (int x = 0; x < kQpBoxes; ++x) {
+                float a = sv[16 * x], c = sv[16 * x + 1];
+#pragma unroll
+                for (int e = 2; e < 16; e += 2) {
+                    a = fmaxf(a, sv[16 * x + e]);
+                    c = fmaxf(c, sv[16 * x + e + 1]);
+                }
+                cand = fmaxf(cand, fmaf(fmaxf(a, c), kf[x], lv[x]));
+            }
+            if (i > 0)
+                take_reference(i - 1);
+            float alpha = 1.f;
+            if (cand > m_ref + kQpGrow) {
+                if (m_ref != -INFINITY)
+                    alpha = ptx::ex2(m_ref - cand);      // (else nothing to rescale)
+                l *= alpha;
+                m_ref = cand;
+            }
+            rows_s[r] = m_ref;
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(settled + 8u * (4 * s + w4));
+            if (__any_sync(kFull, alpha != 1.f)) {
+                // P V of the tile before (and all earlier) must be in O
+                wait(pvdone + 8u * (s ^ 1), (uint32_t)(((i - 1) >> 1) & 1));
+                if (fail)
                     break;
-                }
-                const float mx = fmaxf(cand, rows_s[(half ^ 1) * kQpRows + r]);
-                float alpha = 1.f;
-                if (mx > m_ref + kQpGrow) {
-                    if (m_ref != -INFINITY)
-                        alpha = ptx::ex2(m_ref - mx);    // (else nothing to rescale)
-                    l *= alpha;
-                    m_ref = mx;
-                }
-                if (__any_sync(kFull, alpha != 1.f)) {
-                    // P V of the tile before (and all earlier) must be in O
-                    wait(pfree + 8u * (s ^ 1), (uint32_t)(((i - 1) >> 1) & 1));
-                    ptx::tc_fence_after();
-#pragma unroll 1
-                    for (int c = half * (D / 32); c < (half + 1) * (D / 32) && !fail; ++c) {
-                        uint32_t u[16];
-                        ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 16), u);
-                        ptx::tmem_wait_ld();
-                        ptx::tmem_hold16(u);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-                        ptx::tmem_st16(o_tm + lane_tm + (uint32_t)(c * 16), u);
-                    }
-                    ptx::tmem_wait_st();
-                }
-            }
-            if (i >= 2)
-                wait(pfree + 8u * s, (uint32_t)(((i - 2) >> 1) & 1));
-            if (!fail) {
                 ptx::tc_fence_after();
-                const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t u[16];
+                    ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 16), u);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_hold16(u);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+                    ptx::tmem_st16(o_tm + lane_tm + (uint32_t)(c * 16), u);
+                }
+                ptx::tmem_wait_st();
+            }
+            const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
+            float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {                // 32 tokens at a time
                 uint32_t hi[8], lo[8];
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int x = k >> 2;
+                    const int c = 32 * q + 4 * k, x = c >> 4;
                     uint32_t h2[2], r2[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float e0 = ptx::ex2(fmaf(sv[4 * k + 2 * e], kf[x], nref));
-                        const float e1 = ptx::ex2(fmaf(sv[4 * k + 2 * e + 1], kf[x], nref));
+                        const float e0 = ptx::ex2(fmaf(sv[c + 2 * e], kf[x], nref));
+                        const float e1 = ptx::ex2(fmaf(sv[c + 2 * e + 1], kf[x], nref));
                         l4[2 * (k & 1) + e] += e0 + e1;
                         // (11 bits and 2^-24: far below what hi + lo keep)
                         const uint32_t y = ptx::pack_f16x2(e0 * vw[x], e1 * vw[x]);
@@ -559,33 +568,36 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     hi[k] = h2[0] | (h2[1] << 16);
                     lo[k] = ptx::prmt(r2[0], r2[1], 0x7531u);
                 }
-                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-                ptx::tmem_st8(p_tm + lane_tm + (uint32_t)(s * 32 + 8 * half), hi);
-                ptx::tmem_st8(p_tm + lane_tm + (uint32_t)(s * 32 + 16 + 8 * half), lo);
-                const int from = last_tok - tstart;      // tokens of this half
-                if (from > 0 && from < 32) {
-                    // V rows of a 32-token step past the context: their weight
-                    // is 0, but 0 * NaN is NaN (the half's four warps together)
-                    const uint32_t vst = base + (uint32_t)(L::v_off + vsn * L::kStage);
-                    for (int idx = r; idx < (32 - from) * NCH * 8; idx += kQpRows) {
-                        const int t = 32 * half + from + idx / (NCH * 8), c = idx % (NCH * 8);
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         vst + (uint32_t)((t >> 3) * L::kGroup + (c >> 3) * 1024 +
-                                                          (t & 7) * 128 + (c & 7) * 16)),
-                                     "r"(0)
-                                     : "memory");
-                    }
-                    ptx::fence_proxy_async_smem();
-                }
-                ptx::tmem_wait_st();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    ptx::mbar_arrive(pready + 8u * s);
+                ptx::tmem_st8(sa + (uint32_t)(8 * q), hi);
+                ptx::tmem_st8(sa + (uint32_t)(16 + 8 * q), lo);
             }
+            l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+            const int from = last_tok - tstart;          // tokens of this tile
+            if (from < kQpTile && (from & 31) != 0) {
+                // V rows of the last 32-token step past the context: their
+                // weight is 0, but 0 * NaN is NaN
+                const int to = (from + 31) & ~31;
+                const uint32_t vst = base + (uint32_t)(L::v_off + vsn * L::kStage);
+                for (int idx = r; idx < (to - from) * NCH * 8; idx += kQpRows) {
+                    const int t = from + idx / (NCH * 8), c = idx % (NCH * 8);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                     vst + (uint32_t)((t >> 3) * L::kGroup + (c >> 3) * 1024 +
+                                                      (t & 7) * 128 + (c & 7) * 16)),
+                                 "r"(0)
+                                 : "memory");
+                }
+                ptx::fence_proxy_async_smem();
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(pready + 8u * s);
         }
-        wait(pfree + 8u * ((ntiles - 1) & 1), (uint32_t)(((ntiles - 1) >> 1) & 1));
-        // both halves' sums; with a split, the row's reference and sum for the
+        wait(pvdone + 8u * ((ntiles - 1) & 1), (uint32_t)(((ntiles - 1) >> 1) & 1));
+        if (((ntiles - 1) & 1) != half)
+            take_reference(ntiles - 1);
+        // both sets' sums; with a split, the row's reference and sum for the
         // other CTAs (a warp that gave up takes part in the barriers too)
         ptx::barrier_or(1 + w4, 64, false);              // (rows_s has been read)
         rows_s[half * kQpRows + r] = l;
@@ -600,7 +612,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             ptx::tc_fence_after();
             if (p.split == 1) {
                 // (a sum that is not a number, from a non-finite query, stays one)
-                const float inv = l == 0.f ? 0.f : __frcp_rn(l) * (1.f / kQpWeight);
+                const float inv = l == 0.f ? 0.f : __frcp_rn(l);
                 const bool store = r / G < ntok;
                 uint4 *dst = reinterpret_cast<uint4 *>(
                     p.out +
@@ -688,7 +700,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 a[k].w = fmaf(v.w, f, a[k].w);
             }
         }
-        const float inv = sum == 0.f ? 0.f : __frcp_rn(sum) * (1.f / kQpWeight);
+        const float inv = sum == 0.f ? 0.f : __frcp_rn(sum);
         __nv_bfloat16 *dst =
             p.out + ((int64_t)(q0 + tok0 + r / G) * p.num_q_heads + h * G + r % G) * D + 4 * lane;
 #pragma unroll

@@ -14,7 +14,7 @@ logits s_t and values V_t (everything else is fp32 or exact):
             which counts 2^-6: 2^-23, where the largest x_t is at least 1.
             Prefill: hi of 4 bits (half a step 2^-4, or half the quantum 2^-9),
             lo the rest with 3 bits (half a step 2^-3): 2^-7 of x_t or 2^-13,
-            where the largest x_t is at least 2^3, that is 2^-16 of it.
+            where the largest x_t is at least 1.
   output    bf16, half a step: 2^-8 of it.
 
 fp32 accumulation and the exponential add less than 2^-12 of sum p |V|.
@@ -55,7 +55,7 @@ def attention_with_bound(q, kp, vp, ks, vs, tab, lens, cu, scale, prefill):
                 np.abs(K[:, g]).sum(axis=1)[None, :]
             shift = 2 * np.where(seen, dt, 0).max(axis=1, keepdims=True)
             x = p * sc[None, :, g]
-            rel, least = (2.0 ** -7, 2.0 ** -16) if prefill else (2.0 ** -9, 2.0 ** -23)
+            rel, least = (2.0 ** -7, 2.0 ** -13) if prefill else (2.0 ** -9, 2.0 ** -23)
             off = least * x.max(axis=1, keepdims=True) / sc[None, :, g]
             w = p * (rel + shift + EXTRA) + np.where(seen, off, 0)
             tol[q0:q0 + n, h] = w @ np.abs(V[:, g])
