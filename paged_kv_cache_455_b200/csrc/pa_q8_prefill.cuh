@@ -22,12 +22,15 @@
 //              and passes it on to the other set before it goes on to the
 //              exponentials, so one set's exponentials run beside the other's
 //              loads, maximum and waits
-//   warp 8     MMA issue: P_j V_j, then S_{j+2}
+//   warp 8     MMA issue: S_{j+2} once S_j has been read, then P_j V_j
 //   warp 9     TMA of Q and K
 //   warp 10    TMA of V, block scales
 // Tensor memory columns: S buffers of 64 at 0 and 64, O [128, 128 + d), Q hi
-// and lo (d / 4 each, four values per column).  The weights of tile j (hi 16
-// columns, lo 16) take the place of S_j once its rows have been read.
+// and lo (d / 4 each, four values per column).  The weights go through shared
+// memory, where the bf16 queries were: 16-byte units of a row 2 KB apart, so
+// that a warp's stores are consecutive.  (In tensor memory there is room for
+// them only in place of S_j, and then S_{j+2} waits for P_j V_j: a set's logits,
+// softmax and product ran one after the other, 1960 cycles a tile.)
 // The special-function unit bounds it: two exponentials and two conversions
 // per pair of weights are ~1024 cycles a tile, the products 1050.  MEASURE
 //
@@ -74,9 +77,12 @@ struct Q8PrefillSmem {
     static constexpr int scale_off = v_off + kStages * kStage;   // [stage][ks 4, vs 4]
     static constexpr int row_off = scale_off + kStages * 2 * kQpBoxes * 4;   // [2][rows] floats
     static constexpr int bar_off = row_off + 2 * kQpRows * 4;
-    // kfull, kempty, vfull, vempty [stages], pready[2], pvdone[2], sfull[2], qfull, qready,
-    // drain, settled[2][4]
-    static constexpr int kBars = 4 * kStages + 17;
+    // kfull, kempty, vfull, vempty [stages], pready[2], pvdone[2], sfull[2], sfree[2], qfull,
+    // qready, drain, settled[2][4]
+    static constexpr int kBars = 4 * kStages + 19;
+    // a buffer of weights: hi, then lo, [16-token unit][row][16 bytes]
+    static constexpr int kP = 2 * kQpRows * kQpTile;
+    static_assert(2 * kP <= q_bytes, "two buffers of weights where the queries were");
     static constexpr int flag_off = bar_off + 8 * kBars;
     static constexpr int bytes = 1024 + flag_off + 16;
     static_assert(bytes <= kSmemBudget, "shared memory per CTA");
@@ -110,7 +116,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     const uint32_t bars = base + L::bar_off;
     const uint32_t kfull = bars, kempty = kfull + 8 * S, vfull = kempty + 8 * S,
                    vempty = vfull + 8 * S, pready = vempty + 8 * S, pvdone = pready + 16,
-                   sfull = pvdone + 16, qfull = sfull + 16, qready = qfull + 8, drain = qready + 8,
+                   sfull = pvdone + 16, sfree = sfull + 16, qfull = sfree + 16, qready = qfull + 8, drain = qready + 8,
                    settled = drain + 8;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + L::flag_off);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen + L::flag_off + 4);
@@ -160,6 +166,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             ptx::mbar_init(pready + 8 * i, 4);
             ptx::mbar_init(pvdone + 8 * i, 1);
             ptx::mbar_init(sfull + 8 * i, 1);
+            ptx::mbar_init(sfree + 8 * i, 4);
         }
         for (int i = 0; i < 8; ++i)
             ptx::mbar_init(settled + 8 * i, 1);
@@ -331,9 +338,12 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             if (ptx::elect_one()) {
                 for (int t = 0; t < steps; ++t) {
                     const uint64_t at = vd + (uint64_t)((t * 2 * L::kBox) >> 4);
-                    const uint32_t pa0 = s_tm + (uint32_t)(s * 64 + t * 8);
-                    ptx::umma_f8_ts(o_tm, pa0, at, IDESC_HI, j > 0 || t > 0);
-                    ptx::umma_f8_ts(o_tm, pa0 + 16, at, IDESC_LO, true);
+                    const uint32_t pa0 = base + (uint32_t)(s * L::kP + t * 2 * 16 * kQpRows);
+                    ptx::umma_f8_ss(o_tm, ptx::umma_desc_plain(pa0, 16 * kQpRows, 128), at,
+                                    IDESC_HI, j > 0 || t > 0);
+                    ptx::umma_f8_ss(o_tm,
+                                    ptx::umma_desc_plain(pa0 + L::kP / 2, 16 * kQpRows, 128), at,
+                                    IDESC_LO, true);
                 }
                 ptx::umma_commit(pvdone + 8u * s);
                 ptx::umma_commit(vempty + 8u * vsn);
@@ -347,15 +357,13 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         if (ok && ntiles > 1 && (ok = ready(kfull + 8u * (1 % S), 0, qready, 0)))
             issue_s(1);
         for (int j = 0; ok && j < ntiles; ++j) {
-            if (!(ok = issue_pv(j)))
-                break;
-            // S_{j+2} goes where the weights of tile j were
             if (j + 2 < ntiles) {
                 if (!(ok = ready(kfull + 8u * ((j + 2) % S), (uint32_t)(((j + 2) / S) & 1),
-                                 pvdone + 8u * (j & 1), (uint32_t)((j >> 1) & 1))))
+                                 sfree + 8u * (j & 1), (uint32_t)((j >> 1) & 1))))
                     break;
                 issue_s(j + 2);
             }
+            ok = issue_pv(j);
         }
         if (!ok) {
             if (lane == 0) {
@@ -485,6 +493,11 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     lv[x] = fmaxf(ptx::lg2(vw[x]), -64.f);
                 }
                 ptx::tmem_wait_ld();
+                // S may be overwritten
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(sfree + 8u * s);
                 ptx::tmem_hold16(u0);
                 ptx::tmem_hold16(u1);
                 ptx::tmem_hold16(u2);
@@ -544,14 +557,20 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 }
                 ptx::tmem_wait_st();
             }
+            // weights of the set's tile before have been used
+            if (i >= 2)
+                wait(pvdone + 8u * s, (uint32_t)(((i - 2) >> 1) & 1));
+            if (fail)
+                break;
             const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
+            const uint32_t pw = base + (uint32_t)(s * L::kP + r * 16);
             float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {                // 32 tokens at a time
-                uint32_t hi[8], lo[8];
+            for (int x = 0; x < kQpBoxes; ++x) {         // 16 tokens at a time
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int c = 32 * q + 4 * k, x = c >> 4;
+                for (int k = 0; k < 4; ++k) {
+                    const int c = 16 * x + 4 * k;
                     uint32_t h2[2], r2[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -568,8 +587,14 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     hi[k] = h2[0] | (h2[1] << 16);
                     lo[k] = ptx::prmt(r2[0], r2[1], 0x7531u);
                 }
-                ptx::tmem_st8(sa + (uint32_t)(8 * q), hi);
-                ptx::tmem_st8(sa + (uint32_t)(16 + 8 * q), lo);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 pw + (uint32_t)(x * 16 * kQpRows)),
+                             "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+                             : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 pw + (uint32_t)(L::kP / 2 + x * 16 * kQpRows)),
+                             "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
+                             : "memory");
             }
             l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
             const int from = last_tok - tstart;          // tokens of this tile
@@ -586,10 +611,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                                  "r"(0)
                                  : "memory");
                 }
-                ptx::fence_proxy_async_smem();
             }
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
+            ptx::fence_proxy_async_smem();
+            ptx::tc_fence_before();                      // (of a rescaled O)
             __syncwarp();
             if (lane == 0)
                 ptx::mbar_arrive(pready + 8u * s);
