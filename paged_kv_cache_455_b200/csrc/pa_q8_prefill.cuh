@@ -22,7 +22,9 @@
 //              and passes it on to the other set before it goes on to the
 //              exponentials, so one set's exponentials run beside the other's
 //              loads, maximum and waits
-//   warp 8     MMA issue: S_{j+2} once S_j has been read, then P_j V_j
+//   warp 8     MMA issue of S_{j+2} once S_j has been read
+//   warp 11    MMA issue of P_j V_j (with one warp for both, the tensor cores
+//              idled a third of the time between its waits)
 //   warp 9     TMA of Q and K
 //   warp 10    TMA of V, block scales
 // Tensor memory columns: S buffers of 64 at 0 and 64, O [128, 128 + d), Q hi
@@ -62,7 +64,7 @@ struct Q8PrefillParams {
 constexpr int kQpRows = 128;             // query rows per CTA
 constexpr int kQpTile = 64;              // tokens per stage
 constexpr int kQpBoxes = kQpTile / 16;
-constexpr int kQpThreads = 352;
+constexpr int kQpThreads = 384;
 constexpr float kQpGrow = 8.f;           // log2 growth that makes a new reference
 
 template <int D>
@@ -78,8 +80,8 @@ struct Q8PrefillSmem {
     static constexpr int row_off = scale_off + kStages * 2 * kQpBoxes * 4;   // [2][rows] floats
     static constexpr int bar_off = row_off + 2 * kQpRows * 4;
     // kfull, kempty, vfull, vempty [stages], pready[2], pvdone[2], sfull[2], sfree[2], qfull,
-    // qready, drain, settled[2][4]
-    static constexpr int kBars = 4 * kStages + 19;
+    // qready, drain[2], settled[2][4]
+    static constexpr int kBars = 4 * kStages + 20;
     // a buffer of weights: hi, then lo, [16-token unit][row][16 bytes]
     static constexpr int kP = 2 * kQpRows * kQpTile;
     static_assert(2 * kP <= q_bytes, "two buffers of weights where the queries were");
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     const uint32_t kfull = bars, kempty = kfull + 8 * S, vfull = kempty + 8 * S,
                    vempty = vfull + 8 * S, pready = vempty + 8 * S, pvdone = pready + 16,
                    sfull = pvdone + 16, sfree = sfull + 16, qfull = sfree + 16, qready = qfull + 8, drain = qready + 8,
-                   settled = drain + 8;
+                   settled = drain + 16;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + L::flag_off);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen + L::flag_off + 4);
 
@@ -173,6 +175,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         ptx::mbar_init(qfull, 1);
         ptx::mbar_init(qready, 8);
         ptx::mbar_init(drain, 1);
+        ptx::mbar_init(drain + 8, 1);
         *abort_flag = 0;
     }
     ptx::fence_mbar_init();
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 ptx::mbar_wait_bounded(full + 8u * (i % S), (uint32_t)((i / S) & 1), kWaitLimitNs);
         }
         __syncwarp();
-    } else if (warp == 8) {
+    } else if (warp == 8 || warp == 11) {
         // ====================================================== MMA issue
         auto ready = [&](uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2) -> bool {
             if (__all_sync(kFull, ptx::mbar_test_wait(b1, p1) && ptx::mbar_test_wait(b2, p2)))
@@ -351,19 +354,20 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             __syncwarp();
             return true;
         };
-        bool ok = ready(qready, 0, kfull, 0);
-        if (ok)
-            issue_s(0);
-        if (ok && ntiles > 1 && (ok = ready(kfull + 8u * (1 % S), 0, qready, 0)))
-            issue_s(1);
-        for (int j = 0; ok && j < ntiles; ++j) {
-            if (j + 2 < ntiles) {
-                if (!(ok = ready(kfull + 8u * ((j + 2) % S), (uint32_t)(((j + 2) / S) & 1),
-                                 sfree + 8u * (j & 1), (uint32_t)((j >> 1) & 1))))
+        bool ok = true;
+        if (warp == 8) {
+            ok = ready(qready, 0, kfull, 0);
+            for (int j = 0; ok && j < ntiles; ++j) {
+                if (j > 0 && !(ok = j < 2 ? ready(kfull + 8u * (j % S), 0, qready, 0)
+                                          : ready(kfull + 8u * (j % S), (uint32_t)((j / S) & 1),
+                                                  sfree + 8u * (j & 1),
+                                                  (uint32_t)(((j - 2) >> 1) & 1))))
                     break;
-                issue_s(j + 2);
+                issue_s(j);
             }
-            ok = issue_pv(j);
+        } else {
+            for (int j = 0; ok && j < ntiles; ++j)
+                ok = issue_pv(j);
         }
         if (!ok) {
             if (lane == 0) {
@@ -371,10 +375,11 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 *abort_flag = 1;
             }
             // products already issued finish before the memory goes
+            const uint32_t mine = drain + (warp == 8 ? 0u : 8u);
             if (ptx::elect_one())
-                ptx::umma_commit(drain);
+                ptx::umma_commit(mine);
             __syncwarp();
-            ptx::mbar_wait_bounded(drain, 0, kWaitLimitNs);
+            ptx::mbar_wait_bounded(mine, 0, kWaitLimitNs);
         }
         __syncwarp();
     } else {
@@ -439,12 +444,13 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                         uint32_t h2[2], l2[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float y0 = ptx::bf16lo_to_f32(w[2 * k + e]) * sigma;
-                            const float y1 = ptx::bf16hi_to_f32(w[2 * k + e]) * sigma;
-                            h2[e] = f32x2_to_e4m3x2(y0, y1);
-                            const uint32_t f = e4m3x2_to_f16x2(h2[e]);
-                            l2[e] = f32x2_to_e4m3x2(y0 - ptx::f16lo_to_f32(f),
-                                                    y1 - ptx::f16hi_to_f32(f));
+                            // (8 bits of a value below 256: exact in f16 but
+                            // far below E4M3's quantum, and so is what is left)
+                            const uint32_t y =
+                                ptx::pack_f16x2(ptx::bf16lo_to_f32(w[2 * k + e]) * sigma,
+                                                ptx::bf16hi_to_f32(w[2 * k + e]) * sigma);
+                            h2[e] = f16x2_to_e4m3x2(y);
+                            l2[e] = f16x2_to_e4m3x2(ptx::sub_f16x2(y, e4m3x2_to_f16x2(h2[e])));
                         }
                         hi[2 * v + k] = h2[0] | (h2[1] << 16);
                         lo[2 * v + k] = l2[0] | (l2[1] << 16);
@@ -538,25 +544,6 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             __syncwarp();
             if (lane == 0)
                 ptx::mbar_arrive(settled + 8u * (4 * s + w4));
-            if (__any_sync(kFull, alpha != 1.f)) {
-                // P V of the tile before (and all earlier) must be in O
-                wait(pvdone + 8u * (s ^ 1), (uint32_t)(((i - 1) >> 1) & 1));
-                if (fail)
-                    break;
-                ptx::tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t u[16];
-                    ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 16), u);
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_hold16(u);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-                    ptx::tmem_st16(o_tm + lane_tm + (uint32_t)(c * 16), u);
-                }
-                ptx::tmem_wait_st();
-            }
             // weights of the set's tile before have been used
             if (i >= 2)
                 wait(pvdone + 8u * s, (uint32_t)(((i - 2) >> 1) & 1));
@@ -613,7 +600,33 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 }
             }
             ptx::fence_proxy_async_smem();
-            ptx::tc_fence_before();                      // (of a rescaled O)
+            if (__any_sync(kFull, alpha != 1.f)) {
+                // O to the new reference, once P V of the tile before (and all
+                // earlier) is in it: by now it mostly is
+                wait(pvdone + 8u * (s ^ 1), (uint32_t)(((i - 1) >> 1) & 1));
+                if (fail)
+                    break;
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint32_t at = o_tm + lane_tm + (uint32_t)(c * 64);
+                    uint32_t u[4][16];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::tmem_ld16(at + (uint32_t)(16 * k), u[k]);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        ptx::tmem_hold16(u[k]);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            u[k][e] = __float_as_uint(__uint_as_float(u[k][e]) * alpha);
+                        ptx::tmem_st16(at + (uint32_t)(16 * k), u[k]);
+                    }
+                }
+                ptx::tmem_wait_st();
+            }
+            ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0)
                 ptx::mbar_arrive(pready + 8u * s);
@@ -642,18 +655,24 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     p.out +
                     ((int64_t)(q0 + tok0 + (store ? r / G : 0)) * p.num_q_heads + h * G + r % G) * D);
 #pragma unroll 1
-                for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
-                    uint32_t u[16], o[8];
-                    ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 16), u);
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_hold16(u);
+                for (int c = half * (D / 128); c < (half + 1) * (D / 128); ++c) {
+                    uint32_t u[4][16];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        o[k] = ptx::pack_bf16x2(__uint_as_float(u[2 * k]) * inv,
-                                                __uint_as_float(u[2 * k + 1]) * inv);
-                    if (store) {
-                        dst[2 * c] = make_uint4(o[0], o[1], o[2], o[3]);
-                        dst[2 * c + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+                    for (int k = 0; k < 4; ++k)
+                        ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 64 + 16 * k), u[k]);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        ptx::tmem_hold16(u[k]);
+                        uint32_t o[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            o[e] = ptx::pack_bf16x2(__uint_as_float(u[k][2 * e]) * inv,
+                                                    __uint_as_float(u[k][2 * e + 1]) * inv);
+                        if (store) {
+                            dst[8 * c + 2 * k] = make_uint4(o[0], o[1], o[2], o[3]);
+                            dst[8 * c + 2 * k + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
                     }
                 }
             } else {
