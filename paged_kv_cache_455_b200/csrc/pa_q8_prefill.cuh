@@ -64,7 +64,10 @@ struct Q8PrefillParams {
 constexpr int kQpRows = 128;             // query rows per CTA
 constexpr int kQpTile = 64;              // tokens per stage
 constexpr int kQpBoxes = kQpTile / 16;
-constexpr int kQpThreads = 384;
+constexpr int kQpSets = 3;              // softmax sets of four warps, on tiles in turn
+constexpr int kQpThreads = 128 * kQpSets + 128;
+constexpr int kQpWarpS = 4 * kQpSets, kQpWarpK = kQpWarpS + 1, kQpWarpV = kQpWarpS + 2,
+              kQpWarpPV = kQpWarpS + 3;
 constexpr float kQpGrow = 8.f;           // log2 growth that makes a new reference
 
 template <int D>
@@ -72,26 +75,25 @@ struct Q8PrefillSmem {
     static constexpr int kGroup = 8 * D;                 // bytes between 8-token groups
     static constexpr int kBox = 16 * D;
     static constexpr int kStage = kQpTile * D;           // K or V of a tile
-    static constexpr int kStages = D == 256 ? 5 : 8;
+    // (V is read about three tiles after K)
+    static constexpr int kK = D == 256 ? 4 : 7, kV = D == 256 ? 6 : 9;
     static constexpr int q_bytes = kQpRows * D * 2;      // Q as it comes (bf16)
     static constexpr int k_off = q_bytes;
-    static constexpr int v_off = k_off + kStages * kStage;
-    static constexpr int scale_off = v_off + kStages * kStage;   // [stage][ks 4, vs 4]
-    static constexpr int row_off = scale_off + kStages * 2 * kQpBoxes * 4;   // [2][rows] floats
+    static constexpr int v_off = k_off + kK * kStage;
+    static constexpr int scale_off = v_off + kV * kStage;   // [stage][ks 4, vs 4]
+    static constexpr int row_off = scale_off + kV * 2 * kQpBoxes * 4;   // [set][rows] floats
     static constexpr int bar_off = row_off + 2 * kQpRows * 4;
-    // kfull, kempty, vfull, vempty [stages], pready[2], pvdone[2], sfull[2], sfree[2], qfull,
-    // qready, drain[2], settled[2][4]
-    static constexpr int kBars = 4 * kStages + 20;
-    // a buffer of weights: hi, then lo, [16-token unit][row][16 bytes]
-    static constexpr int kP = 2 * kQpRows * kQpTile;
-    static_assert(2 * kP <= q_bytes, "two buffers of weights where the queries were");
+    // kfull, kempty [kK], vfull, vempty [kV], pready, pvdone, sfull [sets], sfree[2], qfull, qready,
+    // drain[2], settled[2][4].  (Who waits on a barrier has seen the phase before, or knows that
+    // it is over, so that a parity names one phase: hence a set's own sfull, pready, pvdone.)
+    static constexpr int kBars = 2 * (kK + kV) + 3 * kQpSets + 14;
     static constexpr int flag_off = bar_off + 8 * kBars;
     static constexpr int bytes = 1024 + flag_off + 16;
     static_assert(bytes <= kSmemBudget, "shared memory per CTA");
     // a split's accumulator, [row][D] fp32, goes where the stages were
-    static_assert(kQpRows * D * 4 <= 2 * kStages * kStage, "room for an accumulator");
+    static_assert(kQpRows * D * 4 <= (kK + kV) * kStage, "room for an accumulator");
     static constexpr uint32_t tmem_cols = 512;
-    static_assert(128 + D + D / 2 <= 512, "tensor memory columns");
+    static_assert(192 + D + D / 4 <= 512, "tensor memory columns");
 };
 
 template <int D, int G>
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
 {
     using L = Q8PrefillSmem<D>;
     constexpr int TQ = kQpRows / G;
-    constexpr int S = L::kStages;
+    constexpr int SK = L::kK, SV = L::kV;
     constexpr int NCH = D / 128;                 // 128-byte columns of a token
     constexpr uint32_t IDESC_S = ptx::umma_idesc_f8(128, kQpTile, false, false, false, false);
     constexpr uint32_t IDESC_HI = ptx::umma_idesc_f8(128, D, false, false, false, true);
@@ -116,10 +118,10 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     float *scales = reinterpret_cast<float *>(gen + L::scale_off);
     float *rows_s = reinterpret_cast<float *>(gen + L::row_off);
     const uint32_t bars = base + L::bar_off;
-    const uint32_t kfull = bars, kempty = kfull + 8 * S, vfull = kempty + 8 * S,
-                   vempty = vfull + 8 * S, pready = vempty + 8 * S, pvdone = pready + 16,
-                   sfull = pvdone + 16, sfree = sfull + 16, qfull = sfree + 16, qready = qfull + 8, drain = qready + 8,
-                   settled = drain + 16;
+    const uint32_t kfull = bars, kempty = kfull + 8 * SK, vfull = kempty + 8 * SK,
+                   vempty = vfull + 8 * SV, pready = vempty + 8 * SV, pvdone = pready + 8 * kQpSets,
+                   sfull = pvdone + 8 * kQpSets, sfree = sfull + 8 * kQpSets, qfull = sfree + 16,
+                   qready = qfull + 8, drain = qready + 8, settled = drain + 16;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + L::flag_off);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen + L::flag_off + 4);
 
@@ -129,6 +131,8 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     const int h = rest % p.num_kv_heads;
     const int b = rest / p.num_kv_heads;
 
+    if (tid == 0)
+        ptx::prefetch_tensormap(&tmap_q);
     ptx::grid_wait_prerequisites();
     const int q0 = p.cu_q_lens[b];
     const int n = p.cu_q_lens[b + 1] - q0;
@@ -162,23 +166,30 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     auto boxes = [&](int i) { return min(kQpBoxes, (last_tok - (first + i) * kQpTile + 15) >> 4); };
 
     if (tid == 0) {
-        for (int i = 0; i < 4 * S; ++i)
+        for (int i = 0; i < 2 * (SK + SV); ++i)
             ptx::mbar_init(bars + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kQpSets; ++i) {
             ptx::mbar_init(pready + 8 * i, 4);
             ptx::mbar_init(pvdone + 8 * i, 1);
             ptx::mbar_init(sfull + 8 * i, 1);
-            ptx::mbar_init(sfree + 8 * i, 4);
         }
+        for (int i = 0; i < 2; ++i)
+            ptx::mbar_init(sfree + 8 * i, 4);
         for (int i = 0; i < 8; ++i)
             ptx::mbar_init(settled + 8 * i, 1);
         ptx::mbar_init(qfull, 1);
-        ptx::mbar_init(qready, 8);
+        ptx::mbar_init(qready, 4 * kQpSets);
         ptx::mbar_init(drain, 1);
         ptx::mbar_init(drain + 8, 1);
         *abort_flag = 0;
+        ptx::fence_mbar_init();
+        if (ntiles > 0) {                                // Q, before the block ids are known good
+            ptx::mbar_arrive_expect_tx(qfull, (uint32_t)L::q_bytes);
+            for (int c = 0; c < D / 64; ++c)
+                ptx::tma_load_3d_nohint(base + (uint32_t)(c * kQpRows * 128), &tmap_q, c * 64,
+                                        h * G, q0 + tok0, qfull);
+        }
     }
-    ptx::fence_mbar_init();
     bool bad = false;
     const int32_t *trow = p.block_tables + (int64_t)b * p.max_blocks;
     for (int i = tid; i < nblk; i += kQpThreads) {
@@ -193,31 +204,29 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     bad = __syncthreads_or(bad);
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    const uint32_t s_tm = tmem, o_tm = tmem + 128;
-    const uint32_t qh_tm = o_tm + D, ql_tm = qh_tm + D / 4;
+    const uint32_t s_tm = tmem, p_tm = tmem + 128, o_tm = tmem + 192;
+    const uint32_t qh_tm = o_tm + D;
 
     if (bad) {
-        if (tid == 0)
+        if (tid == 0) {
             report(p.dev_status, PA_DEV_BAD_BLOCK);
+            if (ntiles > 0)                              // no copy may land after the CTA is gone
+                ptx::mbar_wait_bounded(qfull, 0, kWaitLimitNs);
+        }
+        __syncwarp();
     } else if (ntiles == 0) {
         // (a split of more CTAs than tiles)
-    } else if (warp == 9 || warp == 10) {
+    } else if (warp == kQpWarpK || warp == kQpWarpV) {
         // ================================================== TMA producers
         // lane x < 4 issues box x (tokens 16 x ..) of each tile
-        const bool is_k = warp == 9;
+        const bool is_k = warp == kQpWarpK;
         const uint32_t full = is_k ? kfull : vfull, empty = is_k ? kempty : vempty;
         const void *tmap = is_k ? static_cast<const void *>(&tmap_k)
                                 : static_cast<const void *>(&tmap_v);
+        const int S = is_k ? SK : SV;
         bool ok = true;
         if (lane == 0) {
             ptx::prefetch_tensormap(tmap);
-            if (is_k) {
-                ptx::prefetch_tensormap(&tmap_q);
-                ptx::mbar_arrive_expect_tx(qfull, (uint32_t)L::q_bytes);
-                for (int c = 0; c < D / 64; ++c)
-                    ptx::tma_load_3d_nohint(base + (uint32_t)(c * kQpRows * 128), &tmap_q, c * 64,
-                                            h * G, q0 + tok0, qfull);
-            }
         }
         // block ids come 32 at a time, one batch ahead
         auto batch_ids = [&](int bt) {
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 ptx::mbar_wait_bounded(full + 8u * (i % S), (uint32_t)((i / S) & 1), kWaitLimitNs);
         }
         __syncwarp();
-    } else if (warp == 8 || warp == 11) {
+    } else if (warp == kQpWarpS || warp == kQpWarpPV) {
         // ====================================================== MMA issue
         auto ready = [&](uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2) -> bool {
             if (__all_sync(kFull, ptx::mbar_test_wait(b1, p1) && ptx::mbar_test_wait(b2, p2)))
@@ -315,24 +324,28 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             ptx::tc_fence_after();
             const uint32_t d = s_tm + (uint32_t)((j & 1) * 64);
             const uint64_t kd = ptx::umma_desc_sw128(
-                base + (uint32_t)(L::k_off + (j % S) * L::kStage), 16, L::kGroup);
+                base + (uint32_t)(L::k_off + (j % SK) * L::kStage), 16, L::kGroup);
             if (ptx::elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 32; ++kk) {
                     const uint64_t at =
                         kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
                     ptx::umma_f8_ts(d, qh_tm + (uint32_t)(kk * 8), at, IDESC_S, kk > 0);
-                    ptx::umma_f8_ts(d, ql_tm + (uint32_t)(kk * 8), at, IDESC_S, true);
+                    ptx::umma_f8_ss(d,
+                                    ptx::umma_desc_sw128(base + (uint32_t)((kk >> 2) * kQpRows * 128 +
+                                                                           (kk & 3) * 32),
+                                                         16, 1024),
+                                    at, IDESC_S, true);
                 }
-                ptx::umma_commit(sfull + 8u * (j & 1));
-                ptx::umma_commit(kempty + 8u * (j % S));
+                ptx::umma_commit(sfull + 8u * (j % kQpSets));
+                ptx::umma_commit(kempty + 8u * (j % SK));
             }
             __syncwarp();
         };
         auto issue_pv = [&](int j) -> bool {
-            const int s = j & 1, vsn = j % S;
-            if (!ready(pready + 8u * s, (uint32_t)((j >> 1) & 1), vfull + 8u * vsn,
-                       (uint32_t)((j / S) & 1)))
+            const int s = j % kQpSets, vsn = j % SV;
+            if (!ready(pready + 8u * s, (uint32_t)((j / kQpSets) & 1), vfull + 8u * vsn,
+                       (uint32_t)((j / SV) & 1)))
                 return false;
             ptx::tc_fence_after();
             const int steps = (boxes(j) + 1) >> 1;       // 32 tokens each
@@ -341,12 +354,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             if (ptx::elect_one()) {
                 for (int t = 0; t < steps; ++t) {
                     const uint64_t at = vd + (uint64_t)((t * 2 * L::kBox) >> 4);
-                    const uint32_t pa0 = base + (uint32_t)(s * L::kP + t * 2 * 16 * kQpRows);
-                    ptx::umma_f8_ss(o_tm, ptx::umma_desc_plain(pa0, 16 * kQpRows, 128), at,
-                                    IDESC_HI, j > 0 || t > 0);
-                    ptx::umma_f8_ss(o_tm,
-                                    ptx::umma_desc_plain(pa0 + L::kP / 2, 16 * kQpRows, 128), at,
-                                    IDESC_LO, true);
+                    const uint32_t pa = p_tm + (uint32_t)((j & 1) * 32 + t * 8);
+                    ptx::umma_f8_ts(o_tm, pa, at, IDESC_HI, j > 0 || t > 0);
+                    ptx::umma_f8_ts(o_tm, pa + 16, at, IDESC_LO, true);
                 }
                 ptx::umma_commit(pvdone + 8u * s);
                 ptx::umma_commit(vempty + 8u * vsn);
@@ -355,11 +365,11 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             return true;
         };
         bool ok = true;
-        if (warp == 8) {
+        if (warp == kQpWarpS) {
             ok = ready(qready, 0, kfull, 0);
             for (int j = 0; ok && j < ntiles; ++j) {
-                if (j > 0 && !(ok = j < 2 ? ready(kfull + 8u * (j % S), 0, qready, 0)
-                                          : ready(kfull + 8u * (j % S), (uint32_t)((j / S) & 1),
+                if (j > 0 && !(ok = j < 2 ? ready(kfull + 8u * (j % SK), 0, qready, 0)
+                                          : ready(kfull + 8u * (j % SK), (uint32_t)((j / SK) & 1),
                                                   sfree + 8u * (j & 1),
                                                   (uint32_t)(((j - 2) >> 1) & 1))))
                     break;
@@ -375,7 +385,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 *abort_flag = 1;
             }
             // products already issued finish before the memory goes
-            const uint32_t mine = drain + (warp == 8 ? 0u : 8u);
+            const uint32_t mine = drain + (warp == kQpWarpS ? 0u : 8u);
             if (ptx::elect_one())
                 ptx::umma_commit(mine);
             __syncwarp();
@@ -384,7 +394,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         __syncwarp();
     } else {
         // =================================================== softmax warps
-        const int w4 = warp & 3, half = warp >> 2;       // tiles half, half + 2, ...
+        const int w4 = warp & 3, set = warp >> 2;        // tiles set, set + kQpSets, ...
         const int r = w4 * 32 + lane;                    // query row = TMEM lane
         const int pos = min(pos0 + r / G, ctx - 1);
         const uint32_t lane_tm = (uint32_t)(w4 * 32) << 16;
@@ -417,28 +427,34 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                              : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                              : "r"(a));
             };
-            uint32_t top = 0;
+            uint32_t top2 = 0;                           // of the even and the odd elements
 #pragma unroll 8
             for (int u8 = 0; u8 < D / 8; ++u8) {
                 uint32_t w[4];
                 unit(u8, w);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    top = max(top, max(w[k] << 16 & 0x7fffffffu, w[k] & 0x7fff0000u));
+                    top2 = ptx::max_u16x2(top2, w[k] & 0x7fff7fffu);
             }
+            const uint32_t top = max(top2 << 16, top2 & 0x7fff0000u);
             const int ef = (int)(top >> 23);
             // (the sign of the softmax scale goes into Q, so that logit
             // factors are not negative)
             const float sig = __uint_as_float((uint32_t)min(254, 261 - ef) << 23);
             const float sigma = p.scale_log2 < 0.f ? -sig : sig;
             fac = ef < 255 ? p.scale_log2 / sigma : __int_as_float(0x7fc00000);
-#pragma unroll 1
-            for (int c = half * (D / 128); c < (half + 1) * (D / 128); ++c) {
-                uint32_t hi[16], lo[16];
+            constexpr int NQ = (D / 32 + kQpSets - 1) / kQpSets;
+            uint32_t lo[NQ][8];
 #pragma unroll
-                for (int v = 0; v < 8; ++v) {
+            for (int x = 0; x < NQ; ++x) {               // 32 elements at a time
+                const int c = set + x * kQpSets;
+                if (c >= D / 32)
+                    break;
+                uint32_t hi[8];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
                     uint32_t w[4];
-                    unit(c * 8 + v, w);
+                    unit(c * 4 + v, w);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         uint32_t h2[2], l2[2];
@@ -453,17 +469,36 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                             l2[e] = f16x2_to_e4m3x2(ptx::sub_f16x2(y, e4m3x2_to_f16x2(h2[e])));
                         }
                         hi[2 * v + k] = h2[0] | (h2[1] << 16);
-                        lo[2 * v + k] = l2[0] | (l2[1] << 16);
+                        lo[x][2 * v + k] = l2[0] | (l2[1] << 16);
                     }
                 }
-                ptx::tmem_st16(qh_tm + lane_tm + (uint32_t)(c * 16), hi);
-                ptx::tmem_st16(ql_tm + lane_tm + (uint32_t)(c * 16), lo);
+                ptx::tmem_st8(qh_tm + lane_tm + (uint32_t)(c * 8), hi);
             }
+            // the low parts in place of the row's elements, once its three warps
+            // have read them (128-element columns of 16384 bytes, swizzled)
+            ptx::barrier_or(1 + w4, 32 * kQpSets, false);
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) {
+                const int c = set + x * kQpSets;
+                if (c >= D / 32)
+                    break;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     base + (uint32_t)((c >> 2) * kQpRows * 128 + r * 128) +
+                                     ((uint32_t)((2 * (c & 3) + u) ^ (r & 7)) << 4)),
+                                 "r"(lo[x][4 * u]), "r"(lo[x][4 * u + 1]), "r"(lo[x][4 * u + 2]),
+                                 "r"(lo[x][4 * u + 3])
+                                 : "memory");
+            }
+            ptx::fence_proxy_async_smem();
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0)
                 ptx::mbar_arrive(qready);
+        } else {
+            ptx::barrier_or(1 + w4, 32 * kQpSets, false);    // (the others' barrier)
         }
         // the reference that the other set's warp of these rows left with tile
         // i (and with it this warp's sum in the same terms)
@@ -474,17 +509,18 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 l *= ptx::ex2(m_ref - m);
             m_ref = m;
         };
-        for (int i = half; i < ntiles && !fail; i += 2) {
-            const int s = i & 1, vsn = i % S;
-            wait(sfull + 8u * s, (uint32_t)((i >> 1) & 1));
+        for (int i = set; i < ntiles && !fail; i += kQpSets) {
+            const int pb = i % kQpSets, vsn = i % SV;
+            wait(sfull + 8u * pb, (uint32_t)((i / kQpSets) & 1));
             // V is in: so are the tile's block scales
-            wait(vfull + 8u * vsn, (uint32_t)((i / S) & 1));
+            wait(vfull + 8u * vsn, (uint32_t)((i / SV) & 1));
             if (fail)
                 break;
             ptx::tc_fence_after();
             const int tstart = (first + i) * kQpTile;
-            const uint32_t sa = s_tm + lane_tm + (uint32_t)(s * 64);
-            float sv[kQpTile], kf[kQpBoxes], lv[kQpBoxes], vw[kQpBoxes], cand = -INFINITY;
+            const uint32_t sa = s_tm + lane_tm + (uint32_t)((i & 1) * 64);
+            float sv[kQpTile], kf[kQpBoxes], lv[kQpBoxes], cand = -INFINITY;
+            bool scaled = true;                          // V scales that have a logarithm
             {
                 uint32_t u0[16], u1[16], u2[16], u3[16];
                 ptx::tmem_ld16(sa, u0);
@@ -494,16 +530,17 @@ __global__ void __launch_bounds__(kQpThreads, 1)
 #pragma unroll
                 for (int x = 0; x < kQpBoxes; ++x) {
                     const float f = fac * scales[vsn * 2 * kQpBoxes + x];
-                    vw[x] = scales[vsn * 2 * kQpBoxes + kQpBoxes + x];
+                    const float vw = scales[vsn * 2 * kQpBoxes + kQpBoxes + x];
                     kf[x] = f == 0.f ? 1.2e-38f : f;     // (a masked -inf stays one)
-                    lv[x] = fmaxf(ptx::lg2(vw[x]), -64.f);
+                    lv[x] = fmaxf(ptx::lg2(vw), -64.f);
+                    scaled &= vw >= 5.5e-20f && vw < INFINITY;   // 2^-64: as lv says
                 }
                 ptx::tmem_wait_ld();
                 // S may be overwritten
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    ptx::mbar_arrive(sfree + 8u * s);
+                    ptx::mbar_arrive(sfree + 8u * (i & 1));
                 ptx::tmem_hold16(u0);
                 ptx::tmem_hold16(u1);
                 ptx::tmem_hold16(u2);
@@ -523,16 +560,24 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             }
 #pragma unroll
             for (int x = 0; x < kQpBoxes; ++x) {
-                float a = sv[16 * x], c = sv[16 * x + 1];
+                float a = ptx::max3(sv[16 * x], sv[16 * x + 1], sv[16 * x + 2]);
+                float c = ptx::max3(sv[16 * x + 3], sv[16 * x + 4], sv[16 * x + 5]);
 #pragma unroll
-                for (int e = 2; e < 16; e += 2) {
-                    a = fmaxf(a, sv[16 * x + e]);
-                    c = fmaxf(c, sv[16 * x + e + 1]);
+                for (int e = 6; e < 14; e += 4) {
+                    a = ptx::max3(a, sv[16 * x + e], sv[16 * x + e + 1]);
+                    c = ptx::max3(c, sv[16 * x + e + 2], sv[16 * x + e + 3]);
                 }
+                a = ptx::max3(a, sv[16 * x + 14], sv[16 * x + 15]);
                 cand = fmaxf(cand, fmaf(fmaxf(a, c), kf[x], lv[x]));
             }
+            // the set's product before is over (seen before the reference is
+            // passed on: who takes it relies on it, for a parity's meaning below)
+            if (i >= kQpSets)
+                wait(pvdone + 8u * pb, (uint32_t)((i / kQpSets - 1) & 1));
             if (i > 0)
                 take_reference(i - 1);
+            if (fail)
+                break;
             float alpha = 1.f;
             if (cand > m_ref + kQpGrow) {
                 if (m_ref != -INFINITY)
@@ -543,47 +588,59 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             rows_s[r] = m_ref;
             __syncwarp();
             if (lane == 0)
-                ptx::mbar_arrive(settled + 8u * (4 * s + w4));
-            // weights of the set's tile before have been used
-            if (i >= 2)
-                wait(pvdone + 8u * s, (uint32_t)(((i - 2) >> 1) & 1));
-            if (fail)
-                break;
+                ptx::mbar_arrive(settled + 8u * (4 * (i & 1) + w4));
             const float nref = m_ref == -INFINITY ? 0.f : -m_ref;
-            const uint32_t pw = base + (uint32_t)(s * L::kP + r * 16);
-            float l4[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t hi[16], lo[16];                     // weights, four tokens each
+            // x = 2^(s - m + log2 vs); the row sum takes x / vs, box by box
 #pragma unroll
             for (int x = 0; x < kQpBoxes; ++x) {         // 16 tokens at a time
-                uint32_t hi[4], lo[4];
+                float *v = sv + 16 * x;
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                if (scaled) {
+                    const float2 k2 = make_float2(kf[x], kf[x]);
+                    const float2 n2 = make_float2(nref + lv[x], nref + lv[x]);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 y = ptx::fma2(make_float2(v[e], v[e + 1]), k2, n2);
+                        v[e] = ptx::ex2(y.x);
+                        v[e + 1] = ptx::ex2(y.y);
+                        sum[e >> 1 & 1] = ptx::add2(sum[e >> 1 & 1], make_float2(v[e], v[e + 1]));
+                    }
+                    l = fmaf((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), ptx::ex2(-lv[x]), l);
+                } else {
+                    const float vw = scales[vsn * 2 * kQpBoxes + kQpBoxes + x];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float y = ptx::ex2(fmaf(v[e], kf[x], nref));
+                        l += y;
+                        v[e] = y * vw;
+                    }
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int c = 16 * x + 4 * k;
                     uint32_t h2[2], r2[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float e0 = ptx::ex2(fmaf(sv[c + 2 * e], kf[x], nref));
-                        const float e1 = ptx::ex2(fmaf(sv[c + 2 * e + 1], kf[x], nref));
-                        l4[2 * (k & 1) + e] += e0 + e1;
                         // (11 bits and 2^-24: far below what hi + lo keep)
-                        const uint32_t y = ptx::pack_f16x2(e0 * vw[x], e1 * vw[x]);
+                        const uint32_t y =
+                            ptx::pack_f16x2(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]);
                         h2[e] = f16x2_to_e4m3x2(y);
                         // the rest as E5M2, the upper byte of an f16: rounded
                         // (half away from zero) by an add below it
                         r2[e] = ptx::sub_f16x2(y, e4m3x2_to_f16x2(h2[e])) + 0x00800080u;
                     }
-                    hi[k] = h2[0] | (h2[1] << 16);
-                    lo[k] = ptx::prmt(r2[0], r2[1], 0x7531u);
+                    hi[4 * x + k] = h2[0] | (h2[1] << 16);
+                    lo[4 * x + k] = ptx::prmt(r2[0], r2[1], 0x7531u);
                 }
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 pw + (uint32_t)(x * 16 * kQpRows)),
-                             "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
-                             : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 pw + (uint32_t)(L::kP / 2 + x * 16 * kQpRows)),
-                             "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
-                             : "memory");
             }
-            l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+            // the buffer's weights of two tiles ago have been used
+            if (i >= 2)
+                wait(pvdone + 8u * ((i - 2) % kQpSets), (uint32_t)(((i - 2) / kQpSets) & 1));
+            if (fail)
+                break;
+            ptx::tc_fence_after();
+            ptx::tmem_st16(p_tm + lane_tm + (uint32_t)((i & 1) * 32), hi);
+            ptx::tmem_st16(p_tm + lane_tm + (uint32_t)((i & 1) * 32 + 16), lo);
             const int from = last_tok - tstart;          // tokens of this tile
             if (from < kQpTile && (from & 31) != 0) {
                 // V rows of the last 32-token step past the context: their
@@ -598,50 +655,65 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                                  "r"(0)
                                  : "memory");
                 }
+                ptx::fence_proxy_async_smem();
             }
-            ptx::fence_proxy_async_smem();
             if (__any_sync(kFull, alpha != 1.f)) {
                 // O to the new reference, once P V of the tile before (and all
                 // earlier) is in it: by now it mostly is
-                wait(pvdone + 8u * (s ^ 1), (uint32_t)(((i - 1) >> 1) & 1));
+                wait(pvdone + 8u * ((i - 1) % kQpSets), (uint32_t)(((i - 1) / kQpSets) & 1));
                 if (fail)
                     break;
                 ptx::tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < D / 64; ++c) {
-                    const uint32_t at = o_tm + lane_tm + (uint32_t)(c * 64);
-                    uint32_t u[4][16];
+                const float2 a2 = make_float2(alpha, alpha);
+                uint32_t u[2][2][16];                    // 32 columns, and the next 32
+                const uint32_t at = o_tm + lane_tm;
+                ptx::tmem_ld16(at, u[0][0]);
+                ptx::tmem_ld16(at + 16, u[0][1]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::tmem_ld16(at + (uint32_t)(16 * k), u[k]);
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t (&now)[2][16] = u[c & 1], (&next)[2][16] = u[(c + 1) & 1];
                     ptx::tmem_wait_ld();
+                    ptx::tmem_hold16(now[0]);
+                    ptx::tmem_hold16(now[1]);
+                    if (c + 1 < D / 32) {
+                        ptx::tmem_ld16(at + (uint32_t)(32 * c + 32), next[0]);
+                        ptx::tmem_ld16(at + (uint32_t)(32 * c + 48), next[1]);
+                    }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        ptx::tmem_hold16(u[k]);
+                    for (int k = 0; k < 2; ++k) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            u[k][e] = __float_as_uint(__uint_as_float(u[k][e]) * alpha);
-                        ptx::tmem_st16(at + (uint32_t)(16 * k), u[k]);
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 y = ptx::mul2(make_float2(__uint_as_float(now[k][e]),
+                                                                   __uint_as_float(now[k][e + 1])),
+                                                       a2);
+                            now[k][e] = __float_as_uint(y.x);
+                            now[k][e + 1] = __float_as_uint(y.y);
+                        }
+                        ptx::tmem_st16(at + (uint32_t)(32 * c + 16 * k), now[k]);
                     }
                 }
-                ptx::tmem_wait_st();
             }
+            ptx::tmem_wait_st();
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                ptx::mbar_arrive(pready + 8u * s);
+                ptx::mbar_arrive(pready + 8u * pb);
         }
-        wait(pvdone + 8u * ((ntiles - 1) & 1), (uint32_t)(((ntiles - 1) >> 1) & 1));
-        if (((ntiles - 1) & 1) != half)
+        if ((ntiles - 1) % kQpSets == set)
+            wait(pvdone + 8u * set, (uint32_t)(((ntiles - 1) / kQpSets) & 1));
+        else
             take_reference(ntiles - 1);
-        // both sets' sums; with a split, the row's reference and sum for the
+        // the sets' sums; with a split, the row's reference and sum for the
         // other CTAs (a warp that gave up takes part in the barriers too)
-        ptx::barrier_or(1 + w4, 64, false);              // (rows_s has been read)
-        rows_s[half * kQpRows + r] = l;
-        ptx::barrier_or(1 + w4, 64, false);
-        l += rows_s[(half ^ 1) * kQpRows + r];
-        ptx::barrier_or(1 + w4, 64, false);
-        if (half == 0) {
+        ptx::barrier_or(1 + w4, 32 * kQpSets, false);    // (rows_s has been read, O is done)
+        float *sums = reinterpret_cast<float *>(gen);    // (where the queries were)
+        sums[set * kQpRows + r] = l;
+        ptx::barrier_or(1 + w4, 32 * kQpSets, false);
+        l = sums[r];
+#pragma unroll
+        for (int k = 1; k < kQpSets; ++k)
+            l += sums[k * kQpRows + r];
+        if (set == 0) {
             rows_s[r] = m_ref;
             rows_s[kQpRows + r] = l;
         }
@@ -655,14 +727,14 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     p.out +
                     ((int64_t)(q0 + tok0 + (store ? r / G : 0)) * p.num_q_heads + h * G + r % G) * D);
 #pragma unroll 1
-                for (int c = half * (D / 128); c < (half + 1) * (D / 128); ++c) {
-                    uint32_t u[4][16];
+                for (int c = set; c < D / 32; c += kQpSets) {
+                    uint32_t u[2][16];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 64 + 16 * k), u[k]);
+                    for (int k = 0; k < 2; ++k)
+                        ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 32 + 16 * k), u[k]);
                     ptx::tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 2; ++k) {
                         ptx::tmem_hold16(u[k]);
                         uint32_t o[8];
 #pragma unroll
@@ -670,8 +742,8 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                             o[e] = ptx::pack_bf16x2(__uint_as_float(u[k][2 * e]) * inv,
                                                     __uint_as_float(u[k][2 * e + 1]) * inv);
                         if (store) {
-                            dst[8 * c + 2 * k] = make_uint4(o[0], o[1], o[2], o[3]);
-                            dst[8 * c + 2 * k + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+                            dst[4 * c + 2 * k] = make_uint4(o[0], o[1], o[2], o[3]);
+                            dst[4 * c + 2 * k + 1] = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                     }
                 }
@@ -679,7 +751,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 // the accumulator to shared memory, where the stages were
                 // (16-byte unit u of row r at u ^ (r & 31))
 #pragma unroll 1
-                for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
+                for (int c = set; c < D / 16; c += kQpSets) {
                     uint32_t u[16];
                     ptx::tmem_ld16(o_tm + lane_tm + (uint32_t)(c * 16), u);
                     ptx::tmem_wait_ld();
