@@ -80,6 +80,7 @@ extern "C" pa_status pa_prefill_attention_q8(void *out, const void *query,
     p.total_q = total_q;
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads;
+    p.num_seqs = num_seqs;
     p.max_blocks = max_blocks_per_seq;
     p.block_size = block_size;
     p.bs_log2 = bs_log2;

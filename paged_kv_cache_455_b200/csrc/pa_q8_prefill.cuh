@@ -54,7 +54,7 @@ struct Q8PrefillParams {
     int32_t *dev_status;
     int64_t num_blocks;
     int total_q, num_q_heads, num_kv_heads;
-    int max_blocks, block_size, bs_log2;
+    int num_seqs, max_blocks, block_size, bs_log2;
     int ctx_cap;
     int qblocks;             // row blocks per (sequence, KV head)
     int split;               // CTAs (a cluster) per row block
@@ -83,10 +83,10 @@ struct Q8PrefillSmem {
     static constexpr int scale_off = v_off + kV * kStage;   // [stage][ks 4, vs 4]
     static constexpr int row_off = scale_off + kV * 2 * kQpBoxes * 4;   // [set][rows] floats
     static constexpr int bar_off = row_off + 2 * kQpRows * 4;
-    // kfull, kempty [kK], vfull, vempty [kV], pready, pvdone, sfull [sets], sfree[2], qfull, qready,
-    // drain[2], settled[2][4].  (Who waits on a barrier has seen the phase before, or knows that
-    // it is over, so that a parity names one phase: hence a set's own sfull, pready, pvdone.)
-    static constexpr int kBars = 2 * (kK + kV) + 3 * kQpSets + 14;
+    // kfull, kempty [kK], vfull, vempty [kV], pready [sets], pvdone [2 sets], sfull [sets],
+    // sfree[2], qfull, qready, drain[2], settled[2][4].  (Who waits on a barrier has seen the
+    // phase before, or knows that it is over: so a parity names one phase.)
+    static constexpr int kBars = 2 * (kK + kV) + 4 * kQpSets + 14;
     static constexpr int flag_off = bar_off + 8 * kBars;
     static constexpr int bytes = 1024 + flag_off + 16;
     static_assert(bytes <= kSmemBudget, "shared memory per CTA");
@@ -120,20 +120,43 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     const uint32_t bars = base + L::bar_off;
     const uint32_t kfull = bars, kempty = kfull + 8 * SK, vfull = kempty + 8 * SK,
                    vempty = vfull + 8 * SV, pready = vempty + 8 * SV, pvdone = pready + 8 * kQpSets,
-                   sfull = pvdone + 8 * kQpSets, sfree = sfull + 8 * kQpSets, qfull = sfree + 16,
+                   sfull = pvdone + 16 * kQpSets, sfree = sfull + 8 * kQpSets, qfull = sfree + 16,
                    qready = qfull + 8, drain = qready + 8, settled = drain + 16;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + L::flag_off);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen + L::flag_off + 4);
 
     const int rank = blockIdx.x % p.split;               // within the cluster
-    const int qb = blockIdx.x / p.split % p.qblocks;
+    const int qb = p.qblocks - 1 - (int)(blockIdx.x / p.split % p.qblocks);
     const int rest = blockIdx.x / p.split / p.qblocks;
     const int h = rest % p.num_kv_heads;
-    const int b = rest / p.num_kv_heads;
+    int b = rest / p.num_kv_heads;
 
-    if (tid == 0)
+    if (tid == 0) {
         ptx::prefetch_tensormap(&tmap_q);
+        ptx::mbar_init(qfull, 1);
+    } else if (tid >= 32 && tid < 32 + L::kBars) {
+        const uint32_t bar = bars + 8 * (tid - 32);
+        if (bar != qfull)
+            ptx::mbar_init(bar, bar >= pready && bar < pvdone ? 4
+                                : bar >= sfree && bar < qfull ? 4
+                                : bar == qready               ? 4 * kQpSets
+                                                              : 1);
+    } else if (tid == 32 * kQpWarpPV) {
+        *abort_flag = 0;
+    }
+    ptx::fence_mbar_init();
     ptx::grid_wait_prerequisites();
+    if (p.num_seqs <= 32) {
+        // The longest contexts first: sequence b is the one with b longer
+        // ones (ties by index).
+        const int len = lane < p.num_seqs ? p.context_lens[lane] : INT_MIN;
+        int longer = 0;
+        for (int i = 0; i < p.num_seqs; ++i) {
+            const int other = __shfl_sync(kFull, len, i);
+            longer += other > len || (other == len && i < lane);
+        }
+        b = __ffs(__ballot_sync(kFull, lane < p.num_seqs && longer == b)) - 1;
+    }
     const int q0 = p.cu_q_lens[b];
     const int n = p.cu_q_lens[b + 1] - q0;
     const int ctx = p.context_lens[b];
@@ -165,40 +188,22 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     const int ntiles = (int)((int64_t)all_tiles * (rank + 1) / p.split) - first;
     auto boxes = [&](int i) { return min(kQpBoxes, (last_tok - (first + i) * kQpTile + 15) >> 4); };
 
-    if (tid == 0) {
-        for (int i = 0; i < 2 * (SK + SV); ++i)
-            ptx::mbar_init(bars + 8 * i, 1);
-        for (int i = 0; i < kQpSets; ++i) {
-            ptx::mbar_init(pready + 8 * i, 4);
-            ptx::mbar_init(pvdone + 8 * i, 1);
-            ptx::mbar_init(sfull + 8 * i, 1);
-        }
-        for (int i = 0; i < 2; ++i)
-            ptx::mbar_init(sfree + 8 * i, 4);
-        for (int i = 0; i < 8; ++i)
-            ptx::mbar_init(settled + 8 * i, 1);
-        ptx::mbar_init(qfull, 1);
-        ptx::mbar_init(qready, 4 * kQpSets);
-        ptx::mbar_init(drain, 1);
-        ptx::mbar_init(drain + 8, 1);
-        *abort_flag = 0;
-        ptx::fence_mbar_init();
-        if (ntiles > 0) {                                // Q, before the block ids are known good
-            ptx::mbar_arrive_expect_tx(qfull, (uint32_t)L::q_bytes);
-            for (int c = 0; c < D / 64; ++c)
-                ptx::tma_load_3d_nohint(base + (uint32_t)(c * kQpRows * 128), &tmap_q, c * 64,
-                                        h * G, q0 + tok0, qfull);
-        }
+    // Q, before the block ids are known good
+    if (tid == 0 && ntiles > 0) {
+        ptx::mbar_arrive_expect_tx(qfull, (uint32_t)L::q_bytes);
+        for (int c = 0; c < D / 64; ++c)
+            ptx::tma_load_3d_nohint(base + (uint32_t)(c * kQpRows * 128), &tmap_q, c * 64, h * G,
+                                    q0 + tok0, qfull);
+    }
+    if (warp == kQpWarpPV) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_holder), L::tmem_cols);
+        ptx::tmem_relinquish();
     }
     bool bad = false;
     const int32_t *trow = p.block_tables + (int64_t)b * p.max_blocks;
     for (int i = tid; i < nblk; i += kQpThreads) {
         const int id = trow[i];
         bad |= id < 0 || (int64_t)id >= p.num_blocks;
-    }
-    if (warp == 0) {
-        ptx::tmem_alloc(ptx::smem_u32(tmem_holder), L::tmem_cols);
-        ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
     bad = __syncthreads_or(bad);
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     ptx::umma_f8_ts(o_tm, pa, at, IDESC_HI, j > 0 || t > 0);
                     ptx::umma_f8_ts(o_tm, pa + 16, at, IDESC_LO, true);
                 }
-                ptx::umma_commit(pvdone + 8u * s);
+                ptx::umma_commit(pvdone + 8u * (j % (2 * kQpSets)));
                 ptx::umma_commit(vempty + 8u * vsn);
             }
             __syncwarp();
@@ -417,78 +422,72 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         };
         wait(qfull, 0);
         if (!fail) {
-            // this row of Q from its swizzled copy (64-element columns of
-            // 16384 bytes): its largest element, then both parts of this
-            // warp's half of the row
-            auto unit = [&](int u8, uint32_t (&w)[4]) {     // elements 8 u8 .. 8 u8 + 7
-                const uint32_t a = base + (uint32_t)((u8 >> 3) * kQpRows * 128 + r * 128) +
-                                   ((uint32_t)((u8 & 7) ^ (r & 7)) << 4);
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                             : "r"(a));
-            };
-            uint32_t top2 = 0;                           // of the even and the odd elements
-#pragma unroll 8
-            for (int u8 = 0; u8 < D / 8; ++u8) {
-                uint32_t w[4];
-                unit(u8, w);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    top2 = ptx::max_u16x2(top2, w[k] & 0x7fff7fffu);
-            }
-            const uint32_t top = max(top2 << 16, top2 & 0x7fff0000u);
-            const int ef = (int)(top >> 23);
-            // (the sign of the softmax scale goes into Q, so that logit
-            // factors are not negative)
-            const float sig = __uint_as_float((uint32_t)min(254, 261 - ef) << 23);
-            const float sigma = p.scale_log2 < 0.f ? -sig : sig;
-            fac = ef < 255 ? p.scale_log2 / sigma : __int_as_float(0x7fc00000);
+            // this set's part of the row of Q from its swizzled copy (64-element
+            // columns of 16384 bytes), 32 elements at a time
             constexpr int NQ = (D / 32 + kQpSets - 1) / kQpSets;
-            uint32_t lo[NQ][8];
-#pragma unroll
-            for (int x = 0; x < NQ; ++x) {               // 32 elements at a time
-                const int c = set + x * kQpSets;
-                if (c >= D / 32)
-                    break;
-                uint32_t hi[8];
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    uint32_t w[4];
-                    unit(c * 4 + v, w);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t h2[2], l2[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            // (8 bits of a value below 256: exact in f16 but
-                            // far below E4M3's quantum, and so is what is left)
-                            const uint32_t y =
-                                ptx::pack_f16x2(ptx::bf16lo_to_f32(w[2 * k + e]) * sigma,
-                                                ptx::bf16hi_to_f32(w[2 * k + e]) * sigma);
-                            h2[e] = f16x2_to_e4m3x2(y);
-                            l2[e] = f16x2_to_e4m3x2(ptx::sub_f16x2(y, e4m3x2_to_f16x2(h2[e])));
-                        }
-                        hi[2 * v + k] = h2[0] | (h2[1] << 16);
-                        lo[x][2 * v + k] = l2[0] | (l2[1] << 16);
-                    }
-                }
-                ptx::tmem_st8(qh_tm + lane_tm + (uint32_t)(c * 8), hi);
-            }
-            // the low parts in place of the row's elements, once its three warps
-            // have read them (128-element columns of 16384 bytes, swizzled)
-            ptx::barrier_or(1 + w4, 32 * kQpSets, false);
+            uint32_t w[NQ][16];
+            uint32_t top2 = 0;                           // largest of the even, the odd elements
 #pragma unroll
             for (int x = 0; x < NQ; ++x) {
                 const int c = set + x * kQpSets;
                 if (c >= D / 32)
                     break;
 #pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[x][4 * u]), "=r"(w[x][4 * u + 1]), "=r"(w[x][4 * u + 2]),
+                                   "=r"(w[x][4 * u + 3])
+                                 : "r"(base + (uint32_t)((c >> 1) * kQpRows * 128 + r * 128) +
+                                       ((uint32_t)((4 * (c & 1) + u) ^ (r & 7)) << 4)));
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    top2 = ptx::max_u16x2(top2, w[x][k] & 0x7fff7fffu);
+            }
+            // the row's largest exponent; behind the barrier the row has been
+            // read, and its low parts may take its place
+            uint8_t *exps = reinterpret_cast<uint8_t *>(rows_s);
+            exps[set * kQpRows + r] = (uint8_t)(max(top2 << 16, top2) >> 23);
+            ptx::barrier_or(1 + w4, 32 * kQpSets, false);
+            int ef = exps[r];
+#pragma unroll
+            for (int k = 1; k < kQpSets; ++k)
+                ef = max(ef, (int)exps[k * kQpRows + r]);
+            // (the sign of the softmax scale goes into Q, so that logit
+            // factors are not negative)
+            const float sig = __uint_as_float((uint32_t)min(254, 261 - ef) << 23);
+            const float sigma = p.scale_log2 < 0.f ? -sig : sig;
+            fac = ef < 255 ? p.scale_log2 / sigma : __int_as_float(0x7fc00000);
+#pragma unroll
+            for (int x = 0; x < NQ; ++x) {
+                const int c = set + x * kQpSets;
+                if (c >= D / 32)
+                    break;
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t h2[2], l2[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // (8 bits of a value below 256: exact in f16 but
+                        // far below E4M3's quantum, and so is what is left)
+                        const uint32_t y =
+                            ptx::pack_f16x2(ptx::bf16lo_to_f32(w[x][2 * k + e]) * sigma,
+                                            ptx::bf16hi_to_f32(w[x][2 * k + e]) * sigma);
+                        h2[e] = f16x2_to_e4m3x2(y);
+                        l2[e] = f16x2_to_e4m3x2(ptx::sub_f16x2(y, e4m3x2_to_f16x2(h2[e])));
+                    }
+                    hi[k] = h2[0] | (h2[1] << 16);
+                    lo[k] = l2[0] | (l2[1] << 16);
+                }
+                ptx::tmem_st8(qh_tm + lane_tm + (uint32_t)(c * 8), hi);
+                // (128-element columns of 16384 bytes, swizzled)
+#pragma unroll
                 for (int u = 0; u < 2; ++u)
                     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
                                      base + (uint32_t)((c >> 2) * kQpRows * 128 + r * 128) +
                                      ((uint32_t)((2 * (c & 3) + u) ^ (r & 7)) << 4)),
-                                 "r"(lo[x][4 * u]), "r"(lo[x][4 * u + 1]), "r"(lo[x][4 * u + 2]),
-                                 "r"(lo[x][4 * u + 3])
+                                 "r"(lo[4 * u]), "r"(lo[4 * u + 1]), "r"(lo[4 * u + 2]),
+                                 "r"(lo[4 * u + 3])
                                  : "memory");
             }
             ptx::fence_proxy_async_smem();
@@ -500,8 +499,14 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         } else {
             ptx::barrier_or(1 + w4, 32 * kQpSets, false);    // (the others' barrier)
         }
-        // the reference that the other set's warp of these rows left with tile
-        // i (and with it this warp's sum in the same terms)
+        // Product j.  Its barrier's phase before was product j - 6's: a set has
+        // seen that end before it passed on the reference of tile j - 1, and
+        // whoever waits here has taken it (or a later one).
+        auto wait_pv = [&](int j) {
+            wait(pvdone + 8u * (j % (2 * kQpSets)), (uint32_t)((j / (2 * kQpSets)) & 1));
+        };
+        // the reference that another set's warp of these rows left with tile i
+        // (and with it this warp's sum in the same terms)
         auto take_reference = [&](int i) {
             wait(settled + 8u * (4 * (i & 1) + w4), (uint32_t)((i >> 1) & 1));
             const float m = rows_s[r];
@@ -570,16 +575,15 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 a = ptx::max3(a, sv[16 * x + 14], sv[16 * x + 15]);
                 cand = fmaxf(cand, fmaf(fmaxf(a, c), kf[x], lv[x]));
             }
-            // the set's product before is over (seen before the reference is
-            // passed on: who takes it relies on it, for a parity's meaning below)
-            if (i >= kQpSets)
-                wait(pvdone + 8u * pb, (uint32_t)((i / kQpSets - 1) & 1));
             if (i > 0)
                 take_reference(i - 1);
             if (fail)
                 break;
+            // one row of the warp that has to move takes along all that may: O is
+            // rescaled once, and they need not move by themselves soon after
+            const bool move = __any_sync(kFull, cand > m_ref + kQpGrow);
             float alpha = 1.f;
-            if (cand > m_ref + kQpGrow) {
+            if (move && cand > m_ref) {
                 if (m_ref != -INFINITY)
                     alpha = ptx::ex2(m_ref - cand);      // (else nothing to rescale)
                 l *= alpha;
@@ -635,7 +639,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             }
             // the buffer's weights of two tiles ago have been used
             if (i >= 2)
-                wait(pvdone + 8u * ((i - 2) % kQpSets), (uint32_t)(((i - 2) / kQpSets) & 1));
+                wait_pv(i - 2);
             if (fail)
                 break;
             ptx::tc_fence_after();
@@ -657,10 +661,10 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 }
                 ptx::fence_proxy_async_smem();
             }
-            if (__any_sync(kFull, alpha != 1.f)) {
+            if (move && i > 0) {
                 // O to the new reference, once P V of the tile before (and all
                 // earlier) is in it: by now it mostly is
-                wait(pvdone + 8u * ((i - 1) % kQpSets), (uint32_t)(((i - 1) / kQpSets) & 1));
+                wait_pv(i - 1);
                 if (fail)
                     break;
                 ptx::tc_fence_after();
@@ -700,7 +704,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 ptx::mbar_arrive(pready + 8u * pb);
         }
         if ((ntiles - 1) % kQpSets == set)
-            wait(pvdone + 8u * set, (uint32_t)(((ntiles - 1) / kQpSets) & 1));
+            wait_pv(ntiles - 1);
         else
             take_reference(ntiles - 1);
         // the sets' sums; with a split, the row's reference and sum for the
@@ -717,15 +721,13 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             rows_s[r] = m_ref;
             rows_s[kQpRows + r] = l;
         }
-        if (!fail) {
-            ptx::tc_fence_after();
-            if (p.split == 1) {
+        if (p.split == 1) {
+            // a row of the output in shared memory, where the stages were
+            // (16-byte unit u of row r at u ^ (r & 7)), then whole rows out
+            if (!fail) {
+                ptx::tc_fence_after();
                 // (a sum that is not a number, from a non-finite query, stays one)
                 const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-                const bool store = r / G < ntok;
-                uint4 *dst = reinterpret_cast<uint4 *>(
-                    p.out +
-                    ((int64_t)(q0 + tok0 + (store ? r / G : 0)) * p.num_q_heads + h * G + r % G) * D);
 #pragma unroll 1
                 for (int c = set; c < D / 32; c += kQpSets) {
                     uint32_t u[2][16];
@@ -741,13 +743,37 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                         for (int e = 0; e < 8; ++e)
                             o[e] = ptx::pack_bf16x2(__uint_as_float(u[k][2 * e]) * inv,
                                                     __uint_as_float(u[k][2 * e + 1]) * inv);
-                        if (store) {
-                            dst[4 * c + 2 * k] = make_uint4(o[0], o[1], o[2], o[3]);
-                            dst[4 * c + 2 * k + 1] = make_uint4(o[4], o[5], o[6], o[7]);
-                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            asm volatile(
+                                "st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                    base + (uint32_t)(L::k_off + r * D * 2) +
+                                    ((uint32_t)((4 * c + 2 * k + e) ^ (r & 7)) << 4)),
+                                "r"(o[4 * e]), "r"(o[4 * e + 1]), "r"(o[4 * e + 2]),
+                                "r"(o[4 * e + 3])
+                                : "memory");
                     }
                 }
-            } else {
+            }
+            ptx::barrier_or(1 + w4, 32 * kQpSets, false);
+            if (!fail) {
+                constexpr int U = D / 8;                 // 16-byte units of a row
+                constexpr int RW = 32 / U;               // rows a warp stores at a time
+                for (int rr = w4 * 32 + set * RW + lane / U; rr < w4 * 32 + 32;
+                     rr += kQpSets * RW) {
+                    const int u = lane % U;
+                    if (rr / G < ntok) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(
+                            p.out +
+                            ((int64_t)(q0 + tok0 + rr / G) * p.num_q_heads + h * G + rr % G) * D);
+                        dst[u] = *reinterpret_cast<const uint4 *>(
+                            gen + L::k_off + rr * D * 2 + ((u ^ (rr & 7)) << 4));
+                    }
+                }
+            }
+        } else {
+            if (!fail) {
+                ptx::tc_fence_after();
                 // the accumulator to shared memory, where the stages were
                 // (16-byte unit u of row r at u ^ (r & 31))
 #pragma unroll 1
@@ -771,7 +797,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == 0)
+    if (warp == kQpWarpPV)
         ptx::tmem_dealloc(tmem, L::tmem_cols);
     if (p.split == 1) {
         // zeros for an invalid block and for a wait that ran out
