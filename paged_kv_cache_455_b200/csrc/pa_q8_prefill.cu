@@ -89,10 +89,15 @@ extern "C" pa_status pa_prefill_attention_q8(void *out, const void *query,
     p.qblocks = (max_q_len + tq_tokens - 1) / tq_tokens;
     p.scale_log2 = scale * pa::kLog2e;
     const int64_t blocks = (int64_t)num_seqs * num_kv_heads * p.qblocks;
-    // Clusters of up to eight CTAs per row block, as long as that makes at
-    // most four CTAs per SM and leaves each at least four tiles.
+    // Clusters of up to eight CTAs per row block, as long as that leaves each
+    // at least four tiles: what one wave of one CTA per SM holds, and two CTAs
+    // for up to 148 row blocks (their lengths differ, and the second wave fills
+    // what the short ones leave).  A CTA costs ~8 us besides its tiles, so more
+    // waves of smaller parts lose: 8 sequences of 5 tokens over 500-4000, 4
+    // heads of 256, 28 us in clusters of 4 and 52 us in clusters of 8; 32 such
+    // sequences 67 us in single CTAs, 58 us in pairs, 89 us in fours.
     p.split = 1;
-    while (p.split < 8 && blocks * 2 * p.split <= 4 * 148 &&
+    while (p.split < 8 && blocks * (p.split == 1 ? 1 : 2 * p.split) <= 148 &&
            max_context_len / pa::kQpTile >= 4 * 2 * p.split)
         p.split *= 2;
     const int64_t grid = blocks * p.split;
