@@ -490,9 +490,9 @@ pa_status pa_rope_and_cache_q8(void *query_out, int64_t query_out_stride, const 
  * as in pa_decode_attention (pa_decode_workspace_bytes sizes the workspace;
  * without it each sequence is processed by one CTA per group of KV heads).
  * Arithmetic: both tile products on E4M3 tensor cores with the codes as stored
- * and fp32 accumulation; query rows and softmax weights are each carried as
- * two E4M3 parts, as in pa_decode_attention_fp8 (three E5M2 parts for the
- * weights).  A weight includes its block's V scale before it is split, and the
+ * and fp32 accumulation; query rows and softmax weights are each carried in
+ * parts, two of E4M3 for the queries as in pa_decode_attention_fp8 and three of
+ * E5M2 for the weights.  A weight includes its block's V scale before it is split, and the
  * weights are kept relative to the largest so scaled, so that their errors are
  * relative to what contributes most to the output; the row
  * sums use the fp32 weights.
@@ -514,7 +514,9 @@ pa_status pa_decode_attention_q8(void *out, const void *query, const void *k_poo
  * pa_prefill_attention_q8 -- pa_prefill_attention over a block-scaled FP8
  * cache: its definition with K and V replaced by code * scale (also for a few
  * drafted tokens per sequence).  Arguments and errors as there, with k_scales
- * and v_scales as in pa_decode_attention_q8; arithmetic as there too.
+ * and v_scales as in pa_decode_attention_q8.  Arithmetic as there, except that a
+ * weight is carried in two parts, E4M3 and the rest as E5M2: off by 2^-7 of
+ * itself, or by 2^-13 where the largest weight of its row is at least 1.
  */
 pa_status pa_prefill_attention_q8(void *out, const void *query, const int32_t *cu_q_lens,
                                   int total_q, int max_q_len, const void *k_pool,

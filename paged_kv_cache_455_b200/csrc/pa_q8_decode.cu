@@ -137,9 +137,10 @@ extern "C" pa_status pa_decode_attention_q8(void *out, const void *query, const 
                                                             counters_off);
         p.epoch = pa::next_epoch();
         // Pieces of a segment, when all are as long as the longest: from six on
-        // a kernel of its own joins them (eight 8K contexts, 19 pieces: MEASURE
-        // us with it, MEASURE us without; 64 contexts of up to 4K, 3 pieces:
-        // MEASURE us with it, MEASURE us without).
+        // a kernel of its own joins them (8K contexts of 4 KV heads of 256: 4 of
+        // them, 37 pieces, 27.0 us with it and 28.8 us without; 8, 33.4 and 34.8;
+        // 24, 6 pieces, 70.0 and 70.3; 32, 4 to 5 pieces, 89.1 and 88.4; 64
+        // contexts of up to 4K, about 3, 53.2 and 49.2).
         const int64_t segments = num_seqs * (int64_t)p.head_groups;
         p.merge_later = num_seqs <= 32 && L.grid >= 6 * segments;
     }

@@ -17,24 +17,32 @@
 // weight would pass 2^8); row sums take the fp32 weights.  The two products at
 // twice bf16's rate cost as much tensor time as one bf16 product would.
 //
-//   warps 0-7  softmax: two sets of four warps take alternate tiles, one query
-//              row per thread.  A set settles the rows' reference for its tile
-//              and passes it on to the other set before it goes on to the
-//              exponentials, so one set's exponentials run beside the other's
-//              loads, maximum and waits
-//   warp 8     MMA issue of S_{j+2} once S_j has been read
-//   warp 11    MMA issue of P_j V_j (with one warp for both, the tensor cores
-//              idled a third of the time between its waits)
-//   warp 9     TMA of Q and K
-//   warp 10    TMA of V, block scales
-// Tensor memory columns: S buffers of 64 at 0 and 64, O [128, 128 + d), Q hi
-// and lo (d / 4 each, four values per column).  The weights go through shared
-// memory, where the bf16 queries were: 16-byte units of a row 2 KB apart, so
-// that a warp's stores are consecutive.  (In tensor memory there is room for
-// them only in place of S_j, and then S_{j+2} waits for P_j V_j: a set's logits,
-// softmax and product ran one after the other, 1960 cycles a tile.)
-// The special-function unit bounds it: two exponentials and two conversions
-// per pair of weights are ~1024 cycles a tile, the products 1050.  MEASURE
+//   warps 0-11  softmax: three sets of four warps take tiles in turn, one query
+//               row per thread.  A set settles the rows' reference for its tile
+//               and passes it on to the next set before it goes on to the
+//               exponentials, so the loads, maxima and waits of two tiles pass
+//               behind the exponentials of a third
+//   warp 12     MMA issue of S_{j+2} once S_j has been read
+//   warp 15     MMA issue of P_j V_j (with one warp for both, the tensor cores
+//               idled between its waits)
+//   warp 13     TMA of K
+//   warp 14     TMA of V, block scales
+// Tensor memory columns: S buffers of 64 at 0 and 64, two buffers of weights (hi
+// and lo, 16 columns each, four values per column), O [192, 192 + d), Q hi
+// (d / 4).  Q lo stays in shared memory, where the bf16 queries were: of all
+// operands it costs least there.  Cycles of the products alone, per tile at
+// d = 256: all in tensor memory 1025 (no room for it), Q lo in shared memory 1126,
+// the weights in shared memory 1347.
+//
+// What bounds it: the tensor cores' 1126 cycles a tile, and around them the
+// softmax warps (528 cycles a tile of exponentials on each scheduler, as much of
+// conversions beside them) and the rescales, for which the product of the
+// tile waits for that of the tile before.  Measured: 16 sequences' chunks of 512
+// tokens over 1-4K, 16 query and 4 KV heads of 256, 352 us (1.05 PFLOP/s counted
+// once, 2.1 of E4M3 products); a bf16 kernel at cuBLAS's rate would take 226 us.
+// A CTA's start and end (Q converted, the first tiles, the last products, the
+// output) take ~8 us besides, hidden by nothing: one CTA fills an SM's tensor
+// memory.
 //
 // Few query rows (drafted tokens, single chunks) over long contexts leave most
 // SMs idle, and there is no workspace to split into: then a cluster of SPLIT

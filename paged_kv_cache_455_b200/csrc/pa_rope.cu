@@ -10,8 +10,16 @@
 // that the result does not depend on how the compiler fuses them); pairs are
 // (i, i + r / 2), or (2 i, 2 i + 1) when interleaved.
 //
-// Both kernels only move data: they are bound by HBM for prompts and by
-// launch and load latency for single tokens.
+// All three kernels only move data: HBM bounds them for prompts, launch and load
+// latency for single tokens.  Measured, 16 query and 4 KV heads of 256, bf16:
+//   pa_rope_and_cache     prompts, 487 MB read and written: 76 us, 6.4 TB/s (0.98
+//                         of a plain copy's rate); 64 single tokens 2.1 us
+//   pa_rope_and_cache_q8  8K tokens in chunks of up to 512, 205 MB: 45 us, 4.6 TB/s;
+//                         256 single tokens 8.5 us with a copy of the lengths
+//   pa_copy_blocks_q8     3000 blocks of 32 tokens, 8 heads of 128, 394 MB: 59.5 us,
+//                         6.6 TB/s; 48 blocks of 16 tokens 2.3 us
+// What keeps the second from the copy's rate is its chain of loads: a CTA of the
+// cache part finds its sequence, then its block, and only then writes.
 #include <algorithm>
 #include <cstdint>
 
@@ -263,7 +271,10 @@ struct RopeQ8Params {
     int num_q_heads, num_kv_heads;
     int bs_log2;
     int write_ctas;          // CTAs of the cache part; the query part follows
+    int query_rows;          // rows per thread of it, at most kQ8QueryRows
 };
+
+constexpr int kQ8QueryRows = 4;      // query rows per thread
 
 // Two fp32 values to E4M3 codes, `lo` in byte 0 (nearest, ties to even,
 // saturating to +-448, NaN to NaN).
@@ -314,7 +325,7 @@ __device__ __forceinline__ int find_sequence(const int32_t *cu, int n, int bs_lo
 // rows already there if the scale grew, and stores the new codes.  No two
 // CTAs touch the same codes or scale, so there are no atomics and the result
 // does not depend on timing.
-// Query part: 128 threads rotate D / 16 units of 128 / (D / 16) * 2 rows.
+// Query part: 128 threads rotate 128 / (D / 16) rows at a time, query_rows times.
 template <int D, int RPT>
 __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p)
 {
@@ -323,10 +334,12 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
     using V8 = Vec<__nv_bfloat16>;
     // With one new token per sequence this grid writes only in each sequence's
     // last block, of which a decode kernel reads nothing before this grid has
-    // completed: the next kernel may start now.  (A chunk fills more blocks.)
+    // completed: the next kernel may start now.  (A chunk fills more blocks.  And
+    // not before the wait: what an append further ahead wrote may lie in blocks
+    // that are no longer a sequence's last.)
+    pa::ptx::grid_wait_prerequisites();
     if (p.max_q_len == 1)
         pa::ptx::grid_launch_dependents();
-    pa::ptx::grid_wait_prerequisites();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int u = tid % UNITS, rl = tid / UNITS;
     const bool inter = p.rot.interleaved != 0;
@@ -335,37 +348,53 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
 
     if ((int)blockIdx.x >= p.write_ctas) {
         // ---------------------------------------------------- query part
-        constexpr int QR = 2;
+        // all rows are asked for before the first is turned
+        constexpr int QR = kQ8QueryRows;
         const int real = min(p.cu_q_lens[p.num_seqs], p.total_q);
-        const int64_t row0 = (int64_t)((int)blockIdx.x - p.write_ctas) * (RPB * QR) + rl;
+        const int64_t row0 = (int64_t)((int)blockIdx.x - p.write_ctas) * (RPB * p.query_rows) + rl;
+        int64_t t = row0 / p.num_q_heads;
+        int h = (int)(row0 - t * p.num_q_heads);
+        int64_t tok[QR], pos[QR];
+        int head[QR];
+        uint4 a[QR], c[QR];
 #pragma unroll
         for (int i = 0; i < QR; ++i) {
-            const int64_t row = row0 + i * RPB;
-            const int64_t t = row / p.num_q_heads;
-            const int h = (int)(row - t * p.num_q_heads);
-            if (t >= real)
+            tok[i] = i < p.query_rows ? t : real;
+            head[i] = h;
+            a[i] = c[i] = make_uint4(0, 0, 0, 0);
+            pos[i] = 0;
+            if (tok[i] < real) {
+                const uint4 *src =
+                    reinterpret_cast<const uint4 *>(p.query + t * p.q_stride + (int64_t)h * D);
+                a[i] = src[c0];
+                c[i] = src[c1];
+                pos[i] = p.rot.positions[t];
+            }
+            for (h += RPB; h >= p.num_q_heads; h -= p.num_q_heads)
+                ++t;
+        }
+#pragma unroll
+        for (int i = 0; i < QR; ++i) {
+            if (tok[i] >= real)
                 continue;
-            const uint4 *src =
-                reinterpret_cast<const uint4 *>(p.query + t * p.q_stride + (int64_t)h * D);
-            uint4 a = src[c0], b = src[c1];
-            const int64_t pos = p.rot.positions[t];
-            if (pos < 0 || pos >= p.rot.max_position) {
-                if (u == 0 && h == 0)
+            if (pos[i] < 0 || pos[i] >= p.rot.max_position) {
+                if (u == 0 && head[i] == 0)
                     pa::report(p.dev_status, PA_DEV_BAD_POSITION);
-                a = b = make_uint4(0, 0, 0, 0);
+                a[i] = c[i] = make_uint4(0, 0, 0, 0);
             } else if (turned) {
                 Angles<8> ang;
-                ang.load(p.rot, pos, u);
+                ang.load(p.rot, pos[i], u);
                 float xa[8], xb[8];
-                V8::unpack(a, xa);
-                V8::unpack(b, xb);
+                V8::unpack(a[i], xa);
+                V8::unpack(c[i], xb);
                 ang.apply(xa, xb, inter);
-                a = V8::pack(xa);
-                b = V8::pack(xb);
+                a[i] = V8::pack(xa);
+                c[i] = V8::pack(xb);
             }
-            uint4 *dst = reinterpret_cast<uint4 *>(p.query_out + t * p.qo_stride + (int64_t)h * D);
-            dst[c0] = a;
-            dst[c1] = b;
+            uint4 *dst = reinterpret_cast<uint4 *>(p.query_out + tok[i] * p.qo_stride +
+                                                   (int64_t)head[i] * D);
+            dst[c0] = a[i];
+            dst[c1] = c[i];
         }
         return;
     }
@@ -406,25 +435,14 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
         return;
     const int lb = (int)first;
     const int id = p.block_tables[(int64_t)b * p.max_blocks + lb];
-    if (id < 0 || (int64_t)id >= p.num_blocks) {
-        if (tid == 0 && kv == 0 && hx == 0)
-            pa::report(p.dev_status, PA_DEV_BAD_BLOCK);
-        return;
-    }
     const int r0 = max(start - (lb << p.bs_log2), 0);          // new rows [r0, r1) of the block
     const int r1 = min(ctx - (lb << p.bs_log2), bs);
     const int64_t t0 = (int64_t)q0 + (lb << p.bs_log2) - start;   // token of row 0
-    float *scale_at = (kv ? p.v_scales : p.k_scales) + (int64_t)id * p.num_kv_heads + hx;
-    const float old = *scale_at;
-    uint8_t *block = (kv ? p.v_pool : p.k_pool) +
-                     ((int64_t)id * bs * p.num_kv_heads + hx) * D;
-    const int64_t row_bytes = (int64_t)p.num_kv_heads * D;
-
-    float xa[RPT][8], xb[RPT][8];
+    // the rows are asked for before the block's number is looked at
+    uint4 a[RPT], c[RPT];
+    int64_t pos[RPT];
     bool have[RPT];
-    float amax = 0.f;
     {
-        uint4 a[RPT], c[RPT];
         const __nv_bfloat16 *src = kv ? p.value : p.key;
         const int64_t stride = kv ? p.v_stride : p.k_stride;
 #pragma unroll
@@ -432,35 +450,50 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
             const int r = rl + k * RPB;
             have[k] = r >= r0 && r < r1;
             a[k] = c[k] = make_uint4(0, 0, 0, 0);
+            pos[k] = 0;
             if (have[k]) {
                 const uint4 *row =
                     reinterpret_cast<const uint4 *>(src + (t0 + r) * stride + (int64_t)hx * D);
                 a[k] = __ldg(row + c0);
                 c[k] = __ldg(row + c1);
+                if (p.rot.rot > 0)
+                    pos[k] = p.rot.positions[t0 + r];
             }
         }
+    }
+    if (id < 0 || (int64_t)id >= p.num_blocks) {
+        if (tid == 0 && kv == 0 && hx == 0)
+            pa::report(p.dev_status, PA_DEV_BAD_BLOCK);
+        return;
+    }
+    float *scale_at = (kv ? p.v_scales : p.k_scales) + (int64_t)id * p.num_kv_heads + hx;
+    const float old = *scale_at;
+    uint8_t *block = (kv ? p.v_pool : p.k_pool) +
+                     ((int64_t)id * bs * p.num_kv_heads + hx) * D;
+    const int64_t row_bytes = (int64_t)p.num_kv_heads * D;
+
+    float xa[RPT][8], xb[RPT][8];
+    float amax = 0.f;
 #pragma unroll
-        for (int k = 0; k < RPT; ++k) {
-            V8::unpack(a[k], xa[k]);
-            V8::unpack(c[k], xb[k]);
-            if (p.rot.rot > 0 && have[k]) {
-                const int64_t pos = p.rot.positions[t0 + rl + k * RPB];
-                if (pos < 0 || pos >= p.rot.max_position) {
-                    // the token is not stored (its value row neither)
-                    if (u == 0 && kv == 0 && hx == 0)
-                        pa::report(p.dev_status, PA_DEV_BAD_POSITION);
-                    have[k] = false;
-                } else if (turned && kv == 0) {
-                    Angles<8> ang;
-                    ang.load(p.rot, pos, u);
-                    ang.apply(xa[k], xb[k], inter);
-                }
+    for (int k = 0; k < RPT; ++k) {
+        V8::unpack(a[k], xa[k]);
+        V8::unpack(c[k], xb[k]);
+        if (p.rot.rot > 0 && have[k]) {
+            if (pos[k] < 0 || pos[k] >= p.rot.max_position) {
+                // the token is not stored (its value row neither)
+                if (u == 0 && kv == 0 && hx == 0)
+                    pa::report(p.dev_status, PA_DEV_BAD_POSITION);
+                have[k] = false;
+            } else if (turned && kv == 0) {
+                Angles<8> ang;
+                ang.load(p.rot, pos[k], u);
+                ang.apply(xa[k], xb[k], inter);
             }
-            if (have[k]) {
+        }
+        if (have[k]) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    amax = fmaxf(amax, fmaxf(finite_abs(xa[k][e]), finite_abs(xb[k][e])));
-            }
+            for (int e = 0; e < 8; ++e)
+                amax = fmaxf(amax, fmaxf(finite_abs(xa[k][e]), finite_abs(xb[k][e])));
         }
     }
     __shared__ float wmax[4];
@@ -735,7 +768,13 @@ pa_status pa_rope_and_cache_q8(void *query_out, int64_t query_out_stride, const 
     const int64_t write = units * num_kv_heads * 2;
     // nothing to do for the queries when they are not rotated in place
     const bool rotate_q = num_q_heads > 0 && !(rot_dim == 0 && query == query_out);
-    const int rows_per_cta = 128 / (head_dim / 16) * 2;
+    // Four rows a thread once they fill the GPU several times over, one for the
+    // few rows of single tokens: 8K new tokens of 16 query heads of 256 take
+    // 45 us with four and 49 us with two one after the other, 256 tokens 9.6 us
+    // with four and 8.5 us with one.
+    const int64_t query_ctas = (int64_t)total_q * num_q_heads / (128 / (head_dim / 16));
+    p.query_rows = query_ctas >= 148 * 16 * 4 ? kQ8QueryRows : 1;
+    const int rows_per_cta = 128 / (head_dim / 16) * p.query_rows;
     const int64_t qctas =
         rotate_q ? ((int64_t)total_q * num_q_heads + rows_per_cta - 1) / rows_per_cta : 0;
     if (write + qctas > INT32_MAX)
