@@ -493,8 +493,17 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
         if (have[k]) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                amax = fmaxf(amax, fmaxf(finite_abs(xa[k][e]), finite_abs(xb[k][e])));
+                amax = fmaxf(amax, fmaxf(fabsf(xa[k][e]), fabsf(xb[k][e])));   // (not NaN)
         }
+    }
+    if (amax > 3.402823466e38f) {            // an infinity: again, without them
+        amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < RPT; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (have[k])
+                    amax = fmaxf(amax, fmaxf(finite_abs(xa[k][e]), finite_abs(xb[k][e])));
     }
     __shared__ float wmax[4];
 #pragma unroll
@@ -529,7 +538,24 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
     // x / s: for a power of two (every scale this kernel makes) the product
     // with the reciprocal is the same number
     const bool pow2 = (__float_as_uint(s) & 0x807fffffu) == 0 && s >= 0x1p-64f && s <= 0x1p120f;
-    const float inv = __fdiv_rn(1.f, s);
+    if (pow2) {
+        const float inv = __fdiv_rn(1.f, s);
+#pragma unroll
+        for (int k = 0; k < RPT; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xa[k][e] *= inv;
+                xb[k][e] *= inv;
+            }
+    } else {
+#pragma unroll
+        for (int k = 0; k < RPT; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xa[k][e] = __fdiv_rn(xa[k][e], s);
+                xb[k][e] = __fdiv_rn(xb[k][e], s);
+            }
+    }
 #pragma unroll
     for (int k = 0; k < RPT; ++k) {
         if (!have[k])
@@ -538,14 +564,10 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
         uint32_t o[4];
 #pragma unroll
         for (int e = 0; e < 8; e += 4) {
-            float y[4], z[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                y[j] = pow2 ? xa[k][e + j] * inv : __fdiv_rn(xa[k][e + j], s);
-                z[j] = pow2 ? xb[k][e + j] * inv : __fdiv_rn(xb[k][e + j], s);
-            }
-            o[e / 4] = e4m3_pair(y[0], y[1]) | (e4m3_pair(y[2], y[3]) << 16);
-            o[2 + e / 4] = e4m3_pair(z[0], z[1]) | (e4m3_pair(z[2], z[3]) << 16);
+            o[e / 4] = e4m3_pair(xa[k][e], xa[k][e + 1]) |
+                       (e4m3_pair(xa[k][e + 2], xa[k][e + 3]) << 16);
+            o[2 + e / 4] = e4m3_pair(xb[k][e], xb[k][e + 1]) |
+                           (e4m3_pair(xb[k][e + 2], xb[k][e + 3]) << 16);
         }
         *reinterpret_cast<uint2 *>(row + 8 * c0) = make_uint2(o[0], o[1]);
         *reinterpret_cast<uint2 *>(row + 8 * c1) = make_uint2(o[2], o[3]);
