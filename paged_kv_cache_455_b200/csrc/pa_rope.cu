@@ -14,12 +14,14 @@
 // latency for single tokens.  Measured, 16 query and 4 KV heads of 256, bf16:
 //   pa_rope_and_cache     prompts, 487 MB read and written: 76 us, 6.4 TB/s (0.98
 //                         of a plain copy's rate); 64 single tokens 2.1 us
-//   pa_rope_and_cache_q8  8K tokens in chunks of up to 512, 205 MB: 45 us, 4.6 TB/s;
+//   pa_rope_and_cache_q8  8K tokens in chunks of up to 512, 205 MB: 42 us, 4.8 TB/s;
 //                         256 single tokens 8.5 us with a copy of the lengths
 //   pa_copy_blocks_q8     3000 blocks of 32 tokens, 8 heads of 128, 394 MB: 59.5 us,
 //                         6.6 TB/s; 48 blocks of 16 tokens 2.3 us
-// What keeps the second from the copy's rate is its chain of loads: a CTA of the
-// cache part finds its sequence, then its block, and only then writes.
+// What keeps the second from the copy's rate is its chain of loads (a CTA of the
+// cache part finds its sequence, then its block, and only then writes) and its
+// arithmetic: the schedulers issue half of the time.  64 registers a thread for
+// more CTAs per SM spill: 43 us.
 #include <algorithm>
 #include <cstdint>
 

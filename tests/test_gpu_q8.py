@@ -325,3 +325,19 @@ def test_prefill_of_few_rows_over_long_contexts(pa, lens, chunks, hq, hkv, d, bs
     out = c.prefill(pa, status)
     assert int(status.item()) == pa.PA_DEV_BAD_BLOCK
     assert (out[:c.cu[1]] == 0).all() and torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("n,hq,hkv,d,bs", [
+    (40, 12, 3, 128, 16),       # row blocks in pairs of CTAs, more sequences than are sorted
+    (32, 16, 4, 256, 16),       # the most that are, many of one length, some without rows
+    (33, 5, 5, 128, 32),        # single CTAs
+])
+def test_prefill_of_many_sequences(pa, n, hq, hkv, d, bs):
+    rng = np.random.default_rng(n)
+    lens = np.where(rng.random(n) < 0.4, 512, rng.integers(1, 900, n))
+    chunks = np.minimum(lens, rng.integers(0, 9, n))
+    c = Case(n, lens, hq, hkv, d, bs, chunks=chunks)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = c.prefill(pa, status)
+    assert int(status.item()) == 0
+    c.check(out, True)
