@@ -835,9 +835,12 @@ pa_status pa_copy_blocks_q8(void *dst_k_pool, void *dst_v_pool, float *dst_k_sca
     for (int i = 0; i < 4; ++i)
         if (!pa::aligned16(ptrs[i]))
             return PA_ERR_INVALID_ARG;
-    for (const void *ptr : ptrs)
-        if (!pa::device_addressable(ptr))
+    for (int i = 0; i < 9; ++i) {
+        if ((i & 2) && ptrs[i] == ptrs[i - 2])
+            continue;                    // copies within one pool
+        if (!pa::device_addressable(ptrs[i]))
             return PA_ERR_INVALID_ARG;   // e.g. pageable host memory
+    }
     CopyQ8Params p;
     p.src_k = static_cast<const uint8_t *>(src_k_pool);
     p.src_v = static_cast<const uint8_t *>(src_v_pool);

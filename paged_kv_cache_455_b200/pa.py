@@ -400,14 +400,14 @@ def _dense(*tensors) -> None:
             raise ValueError("tensors must be contiguous CUDA tensors of the current device")
 
 
-def _token_rows(t: torch.Tensor, name: str, T: int, d: int, dtype) -> int:
+def _token_rows(t: torch.Tensor, name: str, T: int, d: int, dtype, dev) -> int:
     """Elements between tokens of t [T, heads, d], whose heads are dense."""
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != T or shape[2] != d or t.dtype != dtype or not t.is_cuda or \
-            t.get_device() != _current_device():
+    if t.dim() != 3 or t.dtype != dtype or t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, {d}] of {dtype} "
                          "on the current device")
-    heads = shape[1]
+    rows, heads, width = t.shape
+    if rows != T or width != d:
+        raise ValueError(f"{name} must be [{T}, heads, {d}]")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != d and heads > 1):
         raise ValueError(f"the heads of {name} must be dense")
@@ -420,15 +420,16 @@ def _rope_args(query_out, query, key, value, positions, cos_sin, dtype):
     if key.dim() != 3:
         raise ValueError("key must be [tokens, Hkv, d]")
     T, hkv, d = key.shape
-    ks = _token_rows(key, "key", T, d, dtype)
-    vs = _token_rows(value, "value", T, d, dtype)
+    dev = _current_device() if key.is_cuda else None
+    ks = _token_rows(key, "key", T, d, dtype, dev)
+    vs = _token_rows(value, "value", T, d, dtype, dev)
     if value.shape[1] != hkv:
         raise ValueError("shape mismatch")
     hq = qs = qos = 0
     qp = qop = None
     if query is not None and query_out is not None:
-        qs = _token_rows(query, "query", T, d, dtype)
-        qos = _token_rows(query_out, "query_out", T, d, dtype)
+        qs = _token_rows(query, "query", T, d, dtype, dev)
+        qos = _token_rows(query_out, "query_out", T, d, dtype, dev)
         hq = query.shape[1]
         if query_out.shape[1] != hq:
             raise ValueError("shape mismatch")
@@ -602,23 +603,31 @@ def pa_copy_blocks_q8(dst_k: torch.Tensor, dst_v: torch.Tensor, dst_k_scales: to
     """Copies block src -> dst with its scales for each (src, dst) row of
     block_mapping [P, 2] int64, from the source's block-scaled pools to the
     destination's (the same ones, or either side in pinned host memory)."""
-    for t in (dst_k, dst_v, dst_k_scales, dst_v_scales, src_k, src_v, src_k_scales, src_v_scales):
+    # (within one set of pools, as in sharing and compaction, each is checked once)
+    within = src_k is dst_k and src_v is dst_v and src_k_scales is dst_k_scales and \
+        src_v_scales is dst_v_scales
+    pools = (dst_k, dst_v, dst_k_scales, dst_v_scales)
+    if not within:
+        pools += (src_k, src_v, src_k_scales, src_v_scales)
+    for t in pools:
         if not t.is_contiguous() or not (t.is_cuda or t.is_pinned()):
             raise ValueError("pools and scales must be contiguous CUDA or pinned host tensors")
     _dense(block_mapping)
     if dev_status is not None:
         _dense(dev_status)
     dnb, bs, hkv, d = _q8_pools(dst_k, dst_v, dst_k_scales, dst_v_scales)
-    shape = _q8_pools(src_k, src_v, src_k_scales, src_v_scales)
-    if shape[1:] != (bs, hkv, d):
-        raise ValueError("pool shape mismatch")
+    snb = dnb
+    if not within:
+        snb, *rest = _q8_pools(src_k, src_v, src_k_scales, src_v_scales)
+        if rest != [bs, hkv, d]:
+            raise ValueError("pool shape mismatch")
     pairs = block_mapping.shape
     if block_mapping.dtype != torch.int64 or len(pairs) != 2 or pairs[1] != 2:
         raise ValueError("block_mapping must be int64 [P, 2]")
     _check(lib.pa_copy_blocks_q8(dst_k.data_ptr(), dst_v.data_ptr(), dst_k_scales.data_ptr(),
                                  dst_v_scales.data_ptr(), dnb, src_k.data_ptr(),
                                  src_v.data_ptr(), src_k_scales.data_ptr(),
-                                 src_v_scales.data_ptr(), shape[0], block_mapping.data_ptr(),
+                                 src_v_scales.data_ptr(), snb, block_mapping.data_ptr(),
                                  pairs[0], bs, hkv, d, _ptr(dev_status), _stream(stream)),
            "pa_copy_blocks_q8")
 
