@@ -529,6 +529,36 @@ pa_status pa_prefill_attention_q8(void *out, const void *query, const int32_t *c
                                   void *stream);
 
 /*
+ * pa_rope_and_cache_q8_strided, pa_decode_attention_q8_strided,
+ * pa_prefill_attention_q8_strided -- the three calls above for lengths that lie
+ * context_lens_stride elements apart (>= 0; 0: one length for every sequence),
+ * such as a column of a table of per-sequence numbers: sequence b's is
+ * context_lens[b * context_lens_stride].
+ */
+pa_status pa_rope_and_cache_q8_strided(
+    void *query_out, int64_t query_out_stride, const void *query, int64_t query_stride,
+    const void *key, int64_t key_stride, const void *value, int64_t value_stride, void *k_pool,
+    void *v_pool, float *k_scales, float *v_scales, const int32_t *cu_q_lens, int total_q,
+    int max_q_len, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *context_lens, int64_t context_lens_stride, int num_seqs,
+    const int64_t *positions, const float *cos_sin, int rot_dim, int64_t max_position,
+    int interleaved, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+    int64_t num_blocks, int32_t *dev_status, void *stream);
+pa_status pa_decode_attention_q8_strided(
+    void *out, const void *query, const void *k_pool, const void *v_pool, const float *k_scales,
+    const float *v_scales, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *context_lens, int64_t context_lens_stride, int num_seqs, int max_context_len,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+    float scale, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+pa_status pa_prefill_attention_q8_strided(
+    void *out, const void *query, const int32_t *cu_q_lens, int total_q, int max_q_len,
+    const void *k_pool, const void *v_pool, const float *k_scales, const float *v_scales,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+    int64_t context_lens_stride, int num_seqs, int max_context_len, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
+    int32_t *dev_status, void *stream);
+
+/*
  * pa_copy_blocks_q8 -- pa_copy_blocks and pa_swap_blocks for a block-scaled
  * cache: for every pair i, block block_mapping[2i + 1] of the destination
  * pools and its scales become bit-exact copies of block block_mapping[2i] of

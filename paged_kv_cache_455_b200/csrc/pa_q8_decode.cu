@@ -65,6 +65,20 @@ extern "C" pa_status pa_decode_attention_q8(void *out, const void *query, const 
                                             size_t workspace_bytes, int32_t *dev_status,
                                             void *stream)
 {
+    return pa_decode_attention_q8_strided(out, query, k_pool, v_pool, k_scales, v_scales,
+                                          block_tables, max_blocks_per_seq, context_lens, 1,
+                                          num_seqs, max_context_len, num_q_heads, num_kv_heads,
+                                          head_dim, block_size, num_blocks, scale, workspace,
+                                          workspace_bytes, dev_status, stream);
+}
+
+extern "C" pa_status pa_decode_attention_q8_strided(
+    void *out, const void *query, const void *k_pool, const void *v_pool, const float *k_scales,
+    const float *v_scales, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *context_lens, int64_t context_lens_stride, int num_seqs, int max_context_len,
+    int num_q_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+    float scale, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream)
+{
     if ((head_dim != 128 && head_dim != 256) || (block_size != 16 && block_size != 32) ||
         num_seqs > pa::kQ8MaxSeqs)
         return PA_ERR_UNSUPPORTED;
@@ -77,7 +91,7 @@ extern "C" pa_status pa_decode_attention_q8(void *out, const void *query, const 
         return st;
     if (num_seqs == 0)
         return PA_OK;
-    if (!k_scales || !v_scales)
+    if (!k_scales || !v_scales || context_lens_stride < 0)
         return PA_ERR_INVALID_ARG;
     Launch L;
     std::memset(&L.p, 0, sizeof(L.p));
@@ -88,6 +102,7 @@ extern "C" pa_status pa_decode_attention_q8(void *out, const void *query, const 
     p.v_scales = v_scales;
     p.block_tables = block_tables;
     p.context_lens = context_lens;
+    p.len_stride = context_lens_stride;
     p.dev_status = dev_status;
     p.num_blocks = num_blocks;
     p.num_seqs = num_seqs;

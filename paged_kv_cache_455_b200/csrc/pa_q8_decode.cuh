@@ -77,6 +77,7 @@ struct Q8DecodeParams {
     const __nv_bfloat16 *q;
     const float *k_scales, *v_scales;
     const int32_t *block_tables, *context_lens;
+    int64_t len_stride;      // elements between context_lens
     float *pieces;           // mode 0: two slots per CTA
     unsigned long long *counters;   // mode 0: arrivals at the cut segment that starts in a
                                     // CTA's range, a line each (see segment_arrive)
@@ -153,6 +154,16 @@ struct Q8Walk {
     int ord;         // ordinal of the segment in the batch
 };
 
+// Length of sequence b as the caller gave it, and the length to process.
+__device__ __forceinline__ int q8_len(int b, const Q8DecodeParams &p)
+{
+    return p.context_lens[b * p.len_stride];
+}
+__device__ __forceinline__ int q8_ctx(int b, const Q8DecodeParams &p)
+{
+    return b < p.num_seqs ? eff_ctx(q8_len(b, p), p.ctx_cap) : 0;
+}
+
 __device__ __forceinline__ int q8_tiles(int ctx, const Q8DecodeParams &p)
 {
     return (ctx + (1 << p.tt_log2) - 1) >> p.tt_log2;
@@ -166,7 +177,7 @@ __device__ __forceinline__ void q8_prefix(const Q8DecodeParams &p, int *cbase)
     const int nch = (p.num_seqs + 31) >> 5;
     for (int c = warp; c < nch; c += nwarps) {
         const int b = c * 32 + lane;
-        int t = b < p.num_seqs ? q8_tiles(eff_ctx(p.context_lens[b], p.ctx_cap), p) : 0;
+        int t = q8_tiles(q8_ctx(b, p), p);
         const int n = __popc(__ballot_sync(kFull, t > 0));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -218,7 +229,7 @@ __device__ __forceinline__ Q8Walk q8_walk_at(int g, int weight, const Q8DecodePa
             hi = mid - 1;
     }
     const int b = c * 32 + lane;
-    const int ctx = b < p.num_seqs ? eff_ctx(p.context_lens[b], p.ctx_cap) : 0;
+    const int ctx = q8_ctx(b, p);
     const int nt = q8_tiles(ctx, p);
     int t = nt * p.head_groups;
 #pragma unroll
@@ -255,7 +266,7 @@ __device__ __forceinline__ void q8_walk_next(Q8Walk &w, const Q8DecodeParams &p,
     w.hg = 0;
     for (int b0 = w.b + 1; b0 < p.num_seqs; b0 += 32) {
         const int b = b0 + lane;
-        const int ctx = b < p.num_seqs ? eff_ctx(p.context_lens[b], p.ctx_cap) : 0;
+        const int ctx = q8_ctx(b, p);
         const unsigned some = __ballot_sync(kFull, ctx > 0);
         if (some) {
             const int src = __ffs(some) - 1;
@@ -778,7 +789,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             ptx::red_max_relaxed_gpu_u64(p.counters + (int64_t)blockIdx.x * kLineWords,
                                          (unsigned long long)p.epoch << 32);
         for (int b = blockIdx.x; set == 0 && b < p.num_seqs; b += gridDim.x) {
-            const int len = p.context_lens[b];
+            const int len = q8_len(b, p);
             if (eff_ctx(len, p.ctx_cap) > 0)
                 continue;
             if (len != 0 && tid == 0)
@@ -1291,7 +1302,7 @@ __global__ void __launch_bounds__(kQ8MergeThreads) q8_merge_kernel(const Q8Decod
     const int part = blockIdx.x % parts, rest = blockIdx.x / parts;
     const int h = rest % p.hpc, seg = rest / p.hpc;
     const int b = seg / p.head_groups, hg = seg - b * p.head_groups;
-    const int nt = lane < p.num_seqs ? q8_tiles(eff_ctx(p.context_lens[lane], p.ctx_cap), p) : 0;
+    const int nt = q8_tiles(q8_ctx(lane, p), p);
     // units (see q8_range_begin) up to and with sequence `lane`
     const int size = nt > 0 ? (nt + p.end_tiles) * p.head_groups : 0;
     int incl = size, tiles = nt * p.head_groups;

@@ -50,6 +50,20 @@ extern "C" pa_status pa_prefill_attention_q8(void *out, const void *query,
                                              int64_t num_blocks, float scale, int32_t *dev_status,
                                              void *stream)
 {
+    return pa_prefill_attention_q8_strided(
+        out, query, cu_q_lens, total_q, max_q_len, k_pool, v_pool, k_scales, v_scales,
+        block_tables, max_blocks_per_seq, context_lens, 1, num_seqs, max_context_len, num_q_heads,
+        num_kv_heads, head_dim, block_size, num_blocks, scale, dev_status, stream);
+}
+
+extern "C" pa_status pa_prefill_attention_q8_strided(
+    void *out, const void *query, const int32_t *cu_q_lens, int total_q, int max_q_len,
+    const void *k_pool, const void *v_pool, const float *k_scales, const float *v_scales,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+    int64_t context_lens_stride, int num_seqs, int max_context_len, int num_q_heads,
+    int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
+    int32_t *dev_status, void *stream)
+{
     if (total_q < 0 || max_q_len < 0)
         return PA_ERR_INVALID_ARG;
     if ((head_dim != 128 && head_dim != 256) || (block_size != 16 && block_size != 32))
@@ -66,7 +80,7 @@ extern "C" pa_status pa_prefill_attention_q8(void *out, const void *query,
         return PA_ERR_INVALID_ARG;
     if (nothing)
         return PA_OK;
-    if (!cu_q_lens || !k_scales || !v_scales)
+    if (!cu_q_lens || !k_scales || !v_scales || context_lens_stride < 0)
         return PA_ERR_INVALID_ARG;
     pa::Q8PrefillParams p;
     p.out = static_cast<__nv_bfloat16 *>(out);
@@ -75,6 +89,7 @@ extern "C" pa_status pa_prefill_attention_q8(void *out, const void *query,
     p.cu_q_lens = cu_q_lens;
     p.block_tables = block_tables;
     p.context_lens = context_lens;
+    p.len_stride = context_lens_stride;
     p.dev_status = dev_status;
     p.num_blocks = num_blocks;
     p.total_q = total_q;

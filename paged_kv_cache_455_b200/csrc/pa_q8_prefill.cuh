@@ -59,6 +59,7 @@ struct Q8PrefillParams {
     __nv_bfloat16 *out;
     const float *k_scales, *v_scales;
     const int32_t *cu_q_lens, *block_tables, *context_lens;
+    int64_t len_stride;      // elements between context_lens
     int32_t *dev_status;
     int64_t num_blocks;
     int total_q, num_q_heads, num_kv_heads;
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     if (p.num_seqs <= 32) {
         // The longest contexts first: sequence b is the one with b longer
         // ones (ties by index).
-        const int len = lane < p.num_seqs ? p.context_lens[lane] : INT_MIN;
+        const int len = lane < p.num_seqs ? p.context_lens[lane * p.len_stride] : INT_MIN;
         int longer = 0;
         for (int i = 0; i < p.num_seqs; ++i) {
             const int other = __shfl_sync(kFull, len, i);
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     }
     const int q0 = p.cu_q_lens[b];
     const int n = p.cu_q_lens[b + 1] - q0;
-    const int ctx = p.context_lens[b];
+    const int ctx = p.context_lens[b * p.len_stride];
     const int tok0 = qb * TQ;
     const bool rows_ok = n >= 0 && q0 >= 0 && (int64_t)q0 + n <= p.total_q;
     auto zero_rows = [&](int count) {

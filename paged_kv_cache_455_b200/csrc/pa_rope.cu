@@ -266,6 +266,7 @@ struct RopeQ8Params {
     float *k_scales, *v_scales;
     int64_t q_stride, qo_stride, k_stride, v_stride;   // elements between tokens
     const int32_t *cu_q_lens, *block_tables, *context_lens;
+    int64_t len_stride;      // elements between context_lens
     int32_t *dev_status;
     int64_t num_blocks;
     int64_t ctx_cap;
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
         i = unit - ((p.cu_q_lens[b] >> p.bs_log2) + 2 * b);
     }
     const int q0 = p.cu_q_lens[b], n = p.cu_q_lens[b + 1] - q0;
-    const int ctx = p.context_lens[b];
+    const int ctx = p.context_lens[b * p.len_stride];
     auto bad_sequence = [&](int first_row, int rows, int len) {
         return rows < 0 || first_row < 0 || (int64_t)first_row + rows > p.total_q ||
                rows > p.max_q_len || rows > len || len > p.ctx_cap;
@@ -424,7 +425,8 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
         bool bad = false;
         for (int x = tid; x < p.num_seqs; x += 128) {
             const int a = p.cu_q_lens[x];
-            bad |= bad_sequence(a, p.cu_q_lens[x + 1] - a, p.context_lens[x]);
+            bad |= bad_sequence(a, p.cu_q_lens[x + 1] - a,
+                                p.context_lens[x * p.len_stride]);
         }
         if (bad)
             pa::report(p.dev_status, PA_DEV_BAD_CONTEXT);
@@ -744,8 +746,26 @@ pa_status pa_rope_and_cache_q8(void *query_out, int64_t query_out_stride, const 
                                int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
                                int32_t *dev_status, void *stream)
 {
+    return pa_rope_and_cache_q8_strided(
+        query_out, query_out_stride, query, query_stride, key, key_stride, value, value_stride,
+        k_pool, v_pool, k_scales, v_scales, cu_q_lens, total_q, max_q_len, block_tables,
+        max_blocks_per_seq, context_lens, 1, num_seqs, positions, cos_sin, rot_dim, max_position,
+        interleaved, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, dev_status,
+        stream);
+}
+
+pa_status pa_rope_and_cache_q8_strided(
+    void *query_out, int64_t query_out_stride, const void *query, int64_t query_stride,
+    const void *key, int64_t key_stride, const void *value, int64_t value_stride, void *k_pool,
+    void *v_pool, float *k_scales, float *v_scales, const int32_t *cu_q_lens, int total_q,
+    int max_q_len, const int32_t *block_tables, int max_blocks_per_seq,
+    const int32_t *context_lens, int64_t context_lens_stride, int num_seqs,
+    const int64_t *positions, const float *cos_sin, int rot_dim, int64_t max_position,
+    int interleaved, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+    int64_t num_blocks, int32_t *dev_status, void *stream)
+{
     if (total_q < 0 || num_seqs < 0 || max_q_len < 0 || num_q_heads < 0 || num_kv_heads <= 0 ||
-        num_blocks <= 0 || max_blocks_per_seq <= 0)
+        num_blocks <= 0 || max_blocks_per_seq <= 0 || context_lens_stride < 0)
         return PA_ERR_INVALID_ARG;
     if ((head_dim != 128 && head_dim != 256) || (block_size != 16 && block_size != 32))
         return PA_ERR_UNSUPPORTED;
@@ -775,6 +795,7 @@ pa_status pa_rope_and_cache_q8(void *query_out, int64_t query_out_stride, const 
     p.cu_q_lens = cu_q_lens;
     p.block_tables = block_tables;
     p.context_lens = context_lens;
+    p.len_stride = context_lens_stride;
     p.dev_status = dev_status;
     p.num_blocks = num_blocks;
     p.ctx_cap = (int64_t)max_blocks_per_seq * block_size;

@@ -63,6 +63,13 @@ SIGNATURES = {
                                     _I64, _F, _P, _SZ, _P, _P]),
     "pa_prefill_attention_q8": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I,
                                      _I, _I, _I, _I64, _F, _P, _P]),
+    "pa_rope_and_cache_q8_strided": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P,
+                                          _P, _I, _I, _P, _I, _P, _I64, _I, _P, _P, _I, _I64, _I,
+                                          _I, _I, _I, _I, _I64, _P, _P]),
+    "pa_decode_attention_q8_strided": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _I64, _I, _I, _I,
+                                            _I, _I, _I, _I64, _F, _P, _SZ, _P, _P]),
+    "pa_prefill_attention_q8_strided": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _I, _P, _I64,
+                                             _I, _I, _I, _I, _I, _I, _I64, _F, _P, _P]),
     "pa_copy_blocks_q8": (_I, [_P, _P, _P, _P, _I64, _P, _P, _P, _P, _I64, _P, _I, _I, _I, _I,
                                _P, _P]),
     "pa_status_string": (ctypes.c_char_p, [_I]),
@@ -492,14 +499,17 @@ def _q8_pools(k_pool, v_pool, k_scales, v_scales):
     return shape
 
 
-def _tables(block_tables, context_lens, B) -> int:
-    """Checks the tables of B sequences; returns their width."""
+def _tables(block_tables, context_lens, B):
+    """Checks the tables of B sequences; returns their width and the elements
+    between the lengths (which may be a column of another tensor)."""
     shape = block_tables.shape
     if block_tables.dtype != torch.int32 or len(shape) != 2 or shape[0] != B:
         raise ValueError("block_tables must be int32 [B, max_blocks]")
     if context_lens.dtype != torch.int32 or context_lens.shape != (B,):
         raise ValueError("context_lens must be int32 [B]")
-    return shape[1]
+    if context_lens.get_device() != block_tables.get_device():
+        raise ValueError("context_lens must be a CUDA tensor of the current device")
+    return shape[1], context_lens.stride(0)
 
 
 def pa_rope_and_cache_q8(query_out: Optional[torch.Tensor], query: Optional[torch.Tensor],
@@ -513,25 +523,27 @@ def pa_rope_and_cache_q8(query_out: Optional[torch.Tensor], query: Optional[torc
     float8_e4m3fn) with scales [nb, Hkv] fp32: sequence b appends rows
     cu_q_lens[b] .. cu_q_lens[b + 1] - 1, the last of its context_lens[b]
     cached tokens.  cu_q_lens [B + 1], block_tables [B, max_blocks],
-    context_lens [B] int32."""
+    context_lens [B] int32, the lengths at any stride."""
     rows, rot, (T, hq, hkv, d) = _rope_args(query_out, query, key, value, positions, cos_sin,
                                             torch.bfloat16)
-    _dense(k_pool, v_pool, k_scales, v_scales, cu_q_lens, block_tables, context_lens)
+    _dense(k_pool, v_pool, k_scales, v_scales, cu_q_lens, block_tables)
     if dev_status is not None:
         _dense(dev_status)
     nb, bs, phkv, pd = _q8_pools(k_pool, v_pool, k_scales, v_scales)
     if phkv != hkv or pd != d:
         raise ValueError("pool mismatch")
     B = context_lens.shape[0]
-    width = _tables(block_tables, context_lens, B)
+    width, apart = _tables(block_tables, context_lens, B)
     if cu_q_lens.dtype != torch.int32 or cu_q_lens.shape != (B + 1,):
         raise ValueError("cu_q_lens must be int32 [B + 1]")
-    _check(lib.pa_rope_and_cache_q8(*rows, k_pool.data_ptr(), v_pool.data_ptr(),
-                                    k_scales.data_ptr(), v_scales.data_ptr(),
-                                    cu_q_lens.data_ptr(), T, int(max_q_len),
-                                    block_tables.data_ptr(), width, context_lens.data_ptr(), B,
-                                    *rot, 1 if interleaved else 0, hq, hkv, d, bs, nb,
-                                    _ptr(dev_status), _stream(stream)), "pa_rope_and_cache_q8")
+    _check(lib.pa_rope_and_cache_q8_strided(*rows, k_pool.data_ptr(), v_pool.data_ptr(),
+                                            k_scales.data_ptr(), v_scales.data_ptr(),
+                                            cu_q_lens.data_ptr(), T, int(max_q_len),
+                                            block_tables.data_ptr(), width,
+                                            context_lens.data_ptr(), apart, B, *rot,
+                                            1 if interleaved else 0, hq, hkv, d, bs, nb,
+                                            _ptr(dev_status), _stream(stream)),
+           "pa_rope_and_cache_q8")
 
 
 def pa_decode_attention_q8(out: torch.Tensor, query: torch.Tensor, k_pool: torch.Tensor,
@@ -542,27 +554,28 @@ def pa_decode_attention_q8(out: torch.Tensor, query: torch.Tensor, k_pool: torch
                            dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """out, query [B, Hq, d] bf16; pools [nb, bs, Hkv, d] of E4M3 codes with
     scales [nb, Hkv] fp32; block_tables [B, max_blocks], context_lens [B]
-    int32; workspace as in pa_decode_attention."""
-    _dense(out, query, k_pool, v_pool, k_scales, v_scales, block_tables, context_lens)
+    int32, the lengths at any stride; workspace as in pa_decode_attention."""
+    _dense(out, query, k_pool, v_pool, k_scales, v_scales, block_tables)
     B, hq, d = query.shape
     nb, bs, hkv, pd = _q8_pools(k_pool, v_pool, k_scales, v_scales)
     if out.shape != query.shape or pd != d:
         raise ValueError("shape mismatch")
     if query.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
         raise ValueError("query and out must be bf16")
-    width = _tables(block_tables, context_lens, B)
+    width, apart = _tables(block_tables, context_lens, B)
     ws, ws_bytes = None, 0
     if workspace is not None:
         _dense(workspace)
         ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
     if dev_status is not None:
         _dense(dev_status)
-    _check(lib.pa_decode_attention_q8(out.data_ptr(), query.data_ptr(), k_pool.data_ptr(),
-                                      v_pool.data_ptr(), k_scales.data_ptr(),
-                                      v_scales.data_ptr(), block_tables.data_ptr(), width,
-                                      context_lens.data_ptr(), B, int(max_context_len), hq, hkv,
-                                      d, bs, nb, float(scale), ws, ws_bytes, _ptr(dev_status),
-                                      _stream(stream)), "pa_decode_attention_q8")
+    _check(lib.pa_decode_attention_q8_strided(out.data_ptr(), query.data_ptr(), k_pool.data_ptr(),
+                                              v_pool.data_ptr(), k_scales.data_ptr(),
+                                              v_scales.data_ptr(), block_tables.data_ptr(), width,
+                                              context_lens.data_ptr(), apart, B,
+                                              int(max_context_len), hq, hkv, d, bs, nb,
+                                              float(scale), ws, ws_bytes, _ptr(dev_status),
+                                              _stream(stream)), "pa_decode_attention_q8")
 
 
 def pa_prefill_attention_q8(out: torch.Tensor, query: torch.Tensor, cu_q_lens: torch.Tensor,
@@ -573,7 +586,7 @@ def pa_prefill_attention_q8(out: torch.Tensor, query: torch.Tensor, cu_q_lens: t
                             dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """query/out [total_q, Hq, d] bf16; cu_q_lens [B + 1] int32; pools, scales,
     tables and lengths as in pa_decode_attention_q8."""
-    _dense(out, query, cu_q_lens, k_pool, v_pool, k_scales, v_scales, block_tables, context_lens)
+    _dense(out, query, cu_q_lens, k_pool, v_pool, k_scales, v_scales, block_tables)
     if dev_status is not None:
         _dense(dev_status)
     total_q, hq, d = query.shape
@@ -583,16 +596,18 @@ def pa_prefill_attention_q8(out: torch.Tensor, query: torch.Tensor, cu_q_lens: t
         raise ValueError("shape mismatch")
     if query.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
         raise ValueError("query and out must be bf16")
-    width = _tables(block_tables, context_lens, B)
+    width, apart = _tables(block_tables, context_lens, B)
     if cu_q_lens.dtype != torch.int32 or cu_q_lens.shape != (B + 1,):
         raise ValueError("cu_q_lens must be int32 [B + 1]")
-    _check(lib.pa_prefill_attention_q8(out.data_ptr(), query.data_ptr(), cu_q_lens.data_ptr(),
-                                       total_q, int(max_q_len), k_pool.data_ptr(),
-                                       v_pool.data_ptr(), k_scales.data_ptr(),
-                                       v_scales.data_ptr(), block_tables.data_ptr(), width,
-                                       context_lens.data_ptr(), B, int(max_context_len), hq, hkv,
-                                       d, bs, nb, float(scale), _ptr(dev_status),
-                                       _stream(stream)), "pa_prefill_attention_q8")
+    _check(lib.pa_prefill_attention_q8_strided(out.data_ptr(), query.data_ptr(),
+                                               cu_q_lens.data_ptr(), total_q, int(max_q_len),
+                                               k_pool.data_ptr(), v_pool.data_ptr(),
+                                               k_scales.data_ptr(), v_scales.data_ptr(),
+                                               block_tables.data_ptr(), width,
+                                               context_lens.data_ptr(), apart, B,
+                                               int(max_context_len), hq, hkv, d, bs, nb,
+                                               float(scale), _ptr(dev_status), _stream(stream)),
+           "pa_prefill_attention_q8")
 
 
 def pa_copy_blocks_q8(dst_k: torch.Tensor, dst_v: torch.Tensor, dst_k_scales: torch.Tensor,
