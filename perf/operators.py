@@ -390,8 +390,8 @@ def run(st):
     if op == "rope_q8":
         pa.pa_rope_and_cache_q8(st["q_out"], st["q"], st["k"], st["v"], st["kp"], st["vp"],
                                 st["ks"], st["vs"], st["cu"], st["max_q"], st["tables"],
-                                st["lens"].contiguous(), st["pos"], st["table"],
-                                c["interleaved"], st["status"])
+                                st["lens"], st["pos"], st["table"], c["interleaved"],
+                                st["status"])
         return dict(q=st["q_out"], k=st["kp"].view(F8), v=st["vp"].view(F8), ks=st["ks"],
                     vs=st["vs"])
     if op == "decode_q8":
@@ -405,8 +405,8 @@ def run(st):
         return st["out"]
     if op == "prefill_q8":
         pa.pa_prefill_attention_q8(st["out"], st["q"], st["cu"], st["max_q"], st["kp"], st["vp"],
-                                   st["ks"], st["vs"], st["tables"], st["lens"].contiguous(),
-                                   st["max_ctx"], st["scale"], st["status"])
+                                   st["ks"], st["vs"], st["tables"], st["lens"], st["max_ctx"],
+                                   st["scale"], st["status"])
         return st["out"]
     pa.pa_copy_blocks_q8(st["kp"], st["vp"], st["ks"], st["vs"], st["kp"], st["vp"], st["ks"],
                          st["vs"], st["map"], st["status"])
