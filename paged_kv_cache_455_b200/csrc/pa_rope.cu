@@ -371,7 +371,8 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
                     reinterpret_cast<const uint4 *>(p.query + t * p.q_stride + (int64_t)h * D);
                 a[i] = src[c0];
                 c[i] = src[c1];
-                pos[i] = p.rot.positions[t];
+                if (p.rot.rot > 0)
+                    pos[i] = p.rot.positions[t];
             }
             for (h += RPB; h >= p.num_q_heads; h -= p.num_q_heads)
                 ++t;
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
         for (int i = 0; i < QR; ++i) {
             if (tok[i] >= real)
                 continue;
-            if (pos[i] < 0 || pos[i] >= p.rot.max_position) {
+            if (p.rot.rot > 0 && (pos[i] < 0 || pos[i] >= p.rot.max_position)) {
                 if (u == 0 && head[i] == 0)
                     pa::report(p.dev_status, PA_DEV_BAD_POSITION);
                 a[i] = c[i] = make_uint4(0, 0, 0, 0);
