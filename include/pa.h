@@ -515,8 +515,9 @@ pa_status pa_decode_attention_q8(void *out, const void *query, const void *k_poo
  * cache: its definition with K and V replaced by code * scale (also for a few
  * drafted tokens per sequence).  Arguments and errors as there, with k_scales
  * and v_scales as in pa_decode_attention_q8.  Arithmetic as there, except that a
- * weight is carried in two parts, E4M3 and the rest as E5M2: off by 2^-7 of
- * itself, or by 2^-13 where the largest weight of its row is at least 1.
+ * weight (with its block's V scale) is carried in two parts, E4M3 and the rest
+ * as E5M2: off by at most 2^-7 of itself and the lesser of 2^-18 of its row's
+ * largest and 2^-3 of itself; one below 2^-22 of the largest may be lost.
  */
 pa_status pa_prefill_attention_q8(void *out, const void *query, const int32_t *cu_q_lens,
                                   int total_q, int max_q_len, const void *k_pool,

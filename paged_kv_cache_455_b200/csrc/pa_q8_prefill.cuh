@@ -12,10 +12,13 @@
 // s + log2 vs,
 //     x = vs 2^(s - m) = hi + lo,
 // hi the E4M3 part (4 bits, down to 2^-6, subnormal to 2^-9), lo the rest as
-// E5M2 (3 bits, down to 2^-16):  O += hi V + lo V.  A weight is off by 2^-7 of
-// itself or 2^-13, where the largest weight is at least 1 (m moves only once a
-// weight would pass 2^8); row sums take the fp32 weights.  The two products at
-// twice bf16's rate cost as much tensor time as one bf16 product would.
+// E5M2 (3 bits, down to 2^-14, subnormal to 2^-16):  O += hi V + lo V.  A row's
+// largest weight lies between 2^5 (where a new m puts it) and 2^8.75 (past
+// which m moves).  So a weight x is off by at most 2^-7 x + min(2^-13, 2^-3 x +
+// 2^-17), that is by 2^-18 of the row's largest beside 2^-7 of itself, and only
+// those below 2^-22 of the largest vanish; row sums take the fp32 weights.  The
+// two products at twice bf16's rate cost as much tensor time as one bf16 product
+// would.
 //
 //   warps 0-11  softmax: three sets of four warps take tiles in turn, one query
 //               row per thread.  A set settles the rows' reference for its tile
@@ -77,7 +80,13 @@ constexpr int kQpSets = 3;              // softmax sets of four warps, on tiles 
 constexpr int kQpThreads = 128 * kQpSets + 128;
 constexpr int kQpWarpS = 4 * kQpSets, kQpWarpK = kQpWarpS + 1, kQpWarpV = kQpWarpS + 2,
               kQpWarpPV = kQpWarpS + 3;
-constexpr float kQpGrow = 8.f;           // log2 growth that makes a new reference
+// log2 of a row's largest weight when the row gets a reference, and of the
+// largest one for which it gets no new one (E4M3 ends at 448 = 2^8.8).  The
+// lower, the rarer the moves, and the fewer bits small weights keep: with 0 and
+// 8 a tail of 2^-17 beside a weight of 1 loses a tenth of itself.  5 drafted
+// tokens of 32 sequences of 500-4000, 4 heads of 256: 60.5 us, 56.0 with 0 and
+// 8, 61.5 with 5 and 8; prompts of 1024, 145.7 us, 136.4 and 147.3.
+constexpr float kQpLift = 5.f, kQpGrow = 8.75f;
 
 template <int D>
 struct Q8PrefillSmem {
@@ -592,11 +601,11 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             // rescaled once, and they need not move by themselves soon after
             const bool move = __any_sync(kFull, cand > m_ref + kQpGrow);
             float alpha = 1.f;
-            if (move && cand > m_ref) {
+            if (move && cand - kQpLift > m_ref) {
                 if (m_ref != -INFINITY)
-                    alpha = ptx::ex2(m_ref - cand);      // (else nothing to rescale)
+                    alpha = ptx::ex2(m_ref - (cand - kQpLift));   // (else nothing to rescale)
                 l *= alpha;
-                m_ref = cand;
+                m_ref = cand - kQpLift;
             }
             rows_s[r] = m_ref;
             __syncwarp();
