@@ -135,7 +135,10 @@ pa_status pa_reshape_and_cache(const void *key, const void *value, void *k_pool,
  *                  every (sequence, group of KV heads) is processed by one
  *                  CTA.  Both are exact to the same tolerance.  Contents need
  *                  no initialisation and are garbage afterwards; calls
- *                  sharing a workspace must not run concurrently.
+ *                  sharing a workspace must not run concurrently.  (After
+ *                  PA_DEV_WAIT_TIMEOUT, fill it with zeros before a captured
+ *                  call that uses it is replayed: the counts of a call that
+ *                  lost work stay in it.)
  *   dev_status     device int32 or NULL (see PA_DEV_*).
  */
 pa_status pa_decode_attention(void *out, const void *query, const void *k_pool,
@@ -372,7 +375,9 @@ pa_status pa_swap_blocks(void *dst_k_pool, void *dst_v_pool, int64_t dst_num_blo
  *   word of it needs to start at zero: a call counts the partial results of
  *   a split sequence in counter words tagged with that call's own tag (a
  *   word with another tag counts as zero), and reads partial results only
- *   once its own count is complete.
+ *   once its own count is complete, when it clears the word (a captured call
+ *   keeps its tag and may be replayed; after PA_DEV_WAIT_TIMEOUT capture it
+ *   again first).
  */
 #define PA_STATIC_SCRATCH_BYTES (8u << 20)
 pa_status pa_decode_attention_static(void *out, const void *query, const void *k_pool,

@@ -1404,6 +1404,8 @@ __host__ __device__ constexpr int64_t merge_scratch_bytes(int G, int D, int64_t 
 //     with a compare-and-swap on the value its add left.  A restart erases
 //     the adds other arrivals made to the stale word: each of them sees its
 //     own swap fail on a word of this epoch and adds again.
+// Whoever completes a count clears its word: a captured call keeps its epoch,
+// and its next replay counts from zero again.
 // Every arrival is therefore counted once in this epoch.  The add (or the
 // swap) releases the caller's piece, stored before it, and the last arrival
 // acquires every earlier one.
@@ -2393,6 +2395,10 @@ __global__ void __launch_bounds__(KV8 ? kThreads8 : kThreads, 1)
                 }
                 if (arrived != np)
                     continue;   // a later arrival merges the segment
+                // complete: the count starts again from nothing, also for a
+                // replay of this call, which has the same tag
+                if (lane == 0)
+                    ptx::st_relaxed_gpu_u64(counter_of(p, x0, hl), 0);
                 if (first) {
                     firstS = segS;
                     firstX = x0;
