@@ -472,9 +472,9 @@ pa_status pa_rope_and_cache(void *query_out, int64_t query_out_stride, const voi
  * outside [0, max_position) sets PA_DEV_BAD_POSITION: that token is not cached
  * and its query_out row is zeros.  Two sequences must not append to the same
  * block in one call.
- * With max_q_len 1 the kernel lets the next one on the stream start early
- * (see pa_decode_attention_q8; the pools are not to be given to
- * pa_decode_attention_fp8 as well).
+ * With max_q_len 1 the kernel lets the next one on the stream start early (the
+ * pools are not to be given to pa_decode_attention_fp8, which reads blocks
+ * before this kernel has completed).
  */
 pa_status pa_rope_and_cache_q8(void *query_out, int64_t query_out_stride, const void *query,
                                int64_t query_stride, const void *key, int64_t key_stride,
@@ -501,11 +501,8 @@ pa_status pa_rope_and_cache_q8(void *query_out, int64_t query_out_stride, const 
  * weights are kept relative to the largest so scaled, so that their errors are
  * relative to what contributes most to the output; the row
  * sums use the fp32 weights.
- * Before the kernel ahead on the stream has completed, the kernel reads
- * context_lens, block_tables, and the pool rows and scales of blocks other
- * than each sequence's last one: a kernel ahead that allows an early start
- * must not write those.  pa_rope_and_cache_q8 allows one only when max_q_len
- * is 1, and then writes in last blocks alone.
+ * Unlike pa_decode_attention the kernel reads nothing before the kernel ahead
+ * on the stream has completed: any of its inputs may come from that one.
  */
 pa_status pa_decode_attention_q8(void *out, const void *query, const void *k_pool,
                                  const void *v_pool, const float *k_scales, const float *v_scales,

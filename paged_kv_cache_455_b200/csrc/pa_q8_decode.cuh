@@ -44,10 +44,10 @@
 // accumulators only.
 //
 // Memory bounds it, behind the ends: setting up, the queries and the first tiles
-// take ~3 us of a call, a segment's end ~2 us, a merge ~3 us.  Measured: 64
-// sequences of up to 4K tokens, 16 query and 4 KV heads of 256, 267 MB: 50 us, 5.3
-// TB/s; 8 of 8K, 134 MB: 33 us, 4.1 TB/s; 45 of up to 6K, 64 query and 8 KV heads of
-// 128, 239 MB: 56 us, 4.3 TB/s; one of 100 tokens: 10.5 us.
+// take ~5 us of a call, a segment's end ~2 us, a merge ~3 us.  Measured: 64
+// sequences of up to 4K tokens, 16 query and 4 KV heads of 256, 267 MB: 53.4 us, 5.0
+// TB/s; 8 of 8K, 134 MB: 32.3 us, 4.2 TB/s; 45 of up to 6K, 64 query and 8 KV heads of
+// 128, 239 MB: 57.4 us, 4.2 TB/s; one of 100 tokens: 12.1 us.
 //
 // Work is split as in decode_kernel: every CTA owns a contiguous range of the
 // batch's tiles (mode 0), or whole segments (mode 1); a segment is the run of
@@ -363,7 +363,14 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
-    // lengths and block tables are read before the kernel ahead has completed
+    // What the kernel ahead wrote is visible behind this wait only, and it may
+    // be any of the inputs: lengths that a small kernel raised, blocks that a
+    // chunk's append filled or a copy cloned.  So nothing is read before it.
+    // (Reading lengths, tables and full blocks before it took 49.7 us where this
+    // takes 53.4, and 10.6 us where this takes 12.1; see above.)
+    ptx::grid_wait_prerequisites();
+    if (tid == 0)
+        ptx::grid_launch_dependents();
     q8_prefix(p, cbase);                                // contains __syncthreads
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
@@ -374,8 +381,6 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
     const int R0 = q8_range_begin(blockIdx.x, C, total, units, p, cbase, lane);
     const int R1 = q8_range_begin(blockIdx.x + 1, C, total, units, p, cbase, lane);
     const int nk = R1 - R0;
-    if (tid == 0)
-        ptx::grid_launch_dependents();
     const uint64_t lim = p.wait_ns;
     // Whole warp: true once the phase is complete; false when another warp has
     // given up or the bounded wait ran out.
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                                 : static_cast<const void *>(&tmap_v);
         struct Batch {
             int b, hg, j, ns, n, seg, id;
-            bool active, early;
+            bool active;
         };
         bool ok = true;
         int issued = 0;
@@ -433,7 +438,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
             Q8Walk w = q8_walk_at(R0, 0, p, cbase, lane);
             int seg = 0;
             auto fill = [&](int g) {
-                Batch d = {0, 0, 0, 1, 0, 0, -1, false, false};
+                Batch d = {0, 0, 0, 1, 0, 0, -1, false};
                 int t0 = 0;
 #pragma unroll 1
                 for (int i = 0; i < batch; ++i) {
@@ -452,8 +457,6 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                         t0 = d.j << p.tt_log2;
                         d.n = min(tt, w.ctx - t0);
                         d.active = btok < d.n;
-                        // no row of the sequence's last block
-                        d.early = t0 + tt <= ((w.ctx - 1) & ~(p.block_size - 1));
                     }
                 }
                 // one load for the whole batch, waited for by its first use
@@ -463,32 +466,19 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                 return d;
             };
             Batch cur = fill(R0), nxt;
-            // The kernel ahead may write the last block of every sequence (its
-            // rows and scales): the first tiles up to one with such a block are
-            // fetched before it has completed, the rest after.
-            bool waited = false;
             for (int k0 = 0; ok && k0 < nk; k0 += batch, cur = nxt) {
                 const bool valid = cur.active && cur.id >= 0 && (int64_t)cur.id < p.num_blocks;
                 const int head = cur.hg * hpc + bhead;
                 float ks = 0.f, vs = 0.f;
-                auto load_scales = [&](bool now) {
-                    if (now && valid && !is_k) {
-                        const int64_t at = (int64_t)cur.id * p.num_kv_heads + head;
-                        ks = __ldcg(p.k_scales + at);
-                        vs = __ldcg(p.v_scales + at);
-                    }
-                };
-                load_scales(waited || cur.early);
+                if (valid && !is_k) {
+                    const int64_t at = (int64_t)cur.id * p.num_kv_heads + head;
+                    ks = __ldcg(p.k_scales + at);
+                    vs = __ldcg(p.v_scales + at);
+                }
                 const unsigned vmask = __ballot_sync(kFull, valid);
                 const unsigned bmask = __ballot_sync(kFull, cur.active && !valid);
                 for (int i = 0; i < batch && k0 + i < nk; ++i) {
                     const int k = k0 + i, s = k % S;
-                    if (!waited &&
-                        (k >= S || !__shfl_sync(kFull, (int)cur.early, i << nb_log2))) {
-                        ptx::grid_wait_prerequisites();
-                        waited = true;
-                        load_scales(!cur.early);
-                    }
                     if (__any_sync(kFull, *abort_flag != 0))
                         break;
                     if (k >= S &&
@@ -654,7 +644,6 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
         // element in [128, 256)) and split into hi = e4m3(y) and
         // lo = e4m3(y - hi), as over the per-tensor FP8 cache; they become
         // rows (2 h) G + g and (2 h + 1) G + g of the B operand.
-        ptx::grid_wait_prerequisites();
         bool ok = true;
         if (nk > 0) {
             constexpr int E = D / 32;                    // elements per lane
@@ -781,8 +770,6 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
         // ================================================ softmax, epilogue
         const int set = warp >> 2, w4 = warp & 3, st = tid & 127;
         const int rows = hpc * G;
-        // outputs and the workspace may be in use by the kernel ahead
-        ptx::grid_wait_prerequisites();
         // this CTA's counter starts the call at (epoch, 0), unless an arrival
         // has already counted in it
         if (p.mode == 0 && !p.merge_later && tid == 0)
@@ -1287,7 +1274,8 @@ constexpr int kQ8MaxCtas = 148;   // (a merge's weights have room for so many pi
 // Joins the pieces of every cut segment of a batch of at most 32 sequences:
 // CTA (segment, head, part) sums 128 elements of one head row, warp w taking
 // pieces w, w + 4, ...  Which pieces a segment has follows from the lengths, so
-// that is settled before the decode kernel has completed.
+// that is settled before the decode kernel has completed: this kernel starts
+// behind that one's wait, and so behind whatever wrote the lengths.
 constexpr int kQ8MergeThreads = 128;
 
 __global__ void __launch_bounds__(kQ8MergeThreads) q8_merge_kernel(const Q8DecodeParams p, int ctas,

@@ -335,11 +335,9 @@ __global__ void __launch_bounds__(128) rope_cache_q8_kernel(const RopeQ8Params p
     constexpr int UNITS = D / 16;            // threads per row
     constexpr int RPB = 128 / UNITS;         // rows per pass of the CTA
     using V8 = Vec<__nv_bfloat16>;
-    // With one new token per sequence this grid writes only in each sequence's
-    // last block, of which a decode kernel reads nothing before this grid has
-    // completed: the next kernel may start now.  (A chunk fills more blocks.  And
-    // not before the wait: what an append further ahead wrote may lie in blocks
-    // that are no longer a sequence's last.)
+    // With one new token per sequence the next kernel, a decode mostly, may set
+    // itself up now; it reads nothing before this grid has completed.  (Not before
+    // the wait: a kernel that starts then could run beside one further ahead.)
     pa::ptx::grid_wait_prerequisites();
     if (p.max_q_len == 1)
         pa::ptx::grid_launch_dependents();
