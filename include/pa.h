@@ -49,10 +49,14 @@
  *     after; the query rows are only prefetched into L2 before, which reads
  *     no value): a kernel ahead of them that allows an early start
  *     (griddepcontrol.launch_dependents) must not write those arrays or
- *     rows.  pa_reshape_and_cache, which stores exactly each sequence's
- *     last row, is such a kernel and is safe; kernels that do not allow an
- *     early start, host copies and this library's other kernels need no
- *     care.
+ *     rows.  pa_reshape_and_cache and pa_reshape_and_cache_fp8 are such
+ *     kernels: a decode may follow one directly that stored each sequence's
+ *     last row and no other, and that did not itself follow directly another
+ *     one on these pools (whose rows are not the last any more).  Kernels
+ *     that do not allow an early start (other libraries', most of this one's)
+ *     and host copies need no care: the dependent launch behind them happens
+ *     when all their blocks have ended, which these two reads rely on.  The
+ *     decode over a block-scaled cache reads nothing early.
  */
 #ifndef PA_H_
 #define PA_H_

@@ -1799,10 +1799,6 @@ __global__ void __launch_bounds__(KV8 ? kThreads8 : kThreads, 1)
     const int C = min(total_ctas, max(total, 1));
     const int R0 = range_begin(blockIdx.x, C, total, p, cbase, lane);
     const int R1 = range_begin(blockIdx.x + 1, C, total, p, cbase, lane);
-    // the next kernel on the stream may start its own set-up on SMs this
-    // grid leaves; it waits for this grid to complete before using its results
-    if (threadIdx.x == 0)
-        ptx::grid_launch_dependents();
     // the producer warp: the last warp of the consumers (bf16, f32), the
     // first of the producer warpgroup (FP8)
     const int pw = KV8 ? kMaxHpc * SUBS : hpc;
@@ -2156,6 +2152,12 @@ __global__ void __launch_bounds__(KV8 ? kThreads8 : kThreads, 1)
     float *scores = scores_all + hl * kTile * G;
     // outputs and the workspace may still be in use by the kernel ahead
     ptx::grid_wait_prerequisites();
+    // The next kernel on the stream may start its own set-up on SMs this grid
+    // leaves; it waits for this grid to complete before using its results.  Not
+    // before the wait: a decode behind the next cache write reads early the rows
+    // that the cache write ahead of this kernel has stored.
+    if (threadIdx.x == 0)
+        ptx::grid_launch_dependents();
 
     // Sequences without tiles (length 0 or invalid) get a zero output.
     for (int b = blockIdx.x; sub == 0 && b < p.num_seqs; b += total_ctas) {
