@@ -494,8 +494,8 @@ pa_status pa_rope_and_cache_q8(void *query_out, int64_t query_out_stride, const 
 /*
  * pa_decode_attention_q8 -- pa_decode_attention over a block-scaled FP8 cache:
  * its definition with K and V replaced by code * scale.  query and out are
- * bf16 [B, Hq, d]; k_scales and v_scales device [nb, Hkv] fp32, positive and
- * finite; up to 16384 sequences; other arguments, the workspace and the errors
+ * bf16 [B, Hq, d]; k_scales and v_scales device [nb, Hkv] fp32, from 2^-64 to
+ * 2^120 (the append's lie there); up to 16384 sequences; other arguments, the workspace and the errors
  * as in pa_decode_attention (pa_decode_workspace_bytes sizes the workspace;
  * without it each sequence is processed by one CTA per group of KV heads).
  * Arithmetic: both tile products on E4M3 tensor cores with the codes as stored

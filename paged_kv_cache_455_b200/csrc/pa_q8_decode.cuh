@@ -28,8 +28,9 @@
 // its own, so the factors of 8 come out at the end and all parts have the
 // type's whole range: error 2^-9 of x_t down to x_t = 2^-14 and 2^-23 below,
 // relative to a largest weight of at least 1, so that many small weights next
-// to a large one are not lost.  The row sums take the fp32 weights 2^(s_t - m).
-// Because m follows the weights with their scales, the errors are relative to
+// to a large one are not lost.  The row sums take the fp32 weights 2^(s_t - m)
+// (kept in range by kQ8Bias, and joined by times_2_to, for V scales from 2^-64 to
+// 2^120 in any mixture).  Because m follows the weights with their scales, the errors are relative to
 // what the output is made of, whatever the scales' spread.  A warp needs the
 // maximum itself only for its first tile and when a vote finds a lane past the
 // reference, and accumulators are rescaled only then.
@@ -47,7 +48,7 @@
 // take ~5 us of a call, a segment's end ~2 us, a merge ~3 us.  Measured: 64
 // sequences of up to 4K tokens, 16 query and 4 KV heads of 256, 267 MB: 53.4 us, 5.0
 // TB/s; 8 of 8K, 134 MB: 32.3 us, 4.2 TB/s; 45 of up to 6K, 64 query and 8 KV heads of
-// 128, 239 MB: 57.4 us, 4.2 TB/s; one of 100 tokens: 12.1 us.
+// 128, 239 MB: 59.0 us, 4.1 TB/s; one of 100 tokens: 12.1 us.
 //
 // Work is split as in decode_kernel: every CTA owns a contiguous range of the
 // batch's tiles (mode 0), or whole segments (mode 1); a segment is the run of
@@ -71,6 +72,11 @@ constexpr int kQ8Tile = 128;              // rows of K and V per tile (MMA M)
 constexpr int kQ8MaxSeqs = 16384;         // (the prefix of the tile counts is in shared memory)
 constexpr int kQ8SmemStages = 6 * 32768;  // bytes of the stage ring
 constexpr float kQ8Grow = 15.f;           // log2 growth that makes a rescale
+// References are kept this much (log2) lower, so that weights without their V
+// scale, 2^-120 of the others' with the largest one, and those 2^-30 of them
+// are normal numbers; with the smallest, 2^-64, a million of 2^(64 + 15) still
+// have a finite sum.
+constexpr float kQ8Bias = 24.f;
 
 struct Q8DecodeParams {
     __nv_bfloat16 *out;
@@ -832,7 +838,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                 uint32_t u[2 * G];
                 ptx::tmem_ld<2 * G>(tmem + (uint32_t)((k & 1) * 64 + hl * 2 * G) + lane_tm, u);
                 lv = fmaxf(ptx::lg2(vs), -64.f);
-                room = kQ8Grow - lv;
+                room = kQ8Grow + kQ8Bias - lv;
                 seen = tok < n;
                 ptx::tmem_wait_ld();
                 ptx::tc_fence_before();
@@ -846,7 +852,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                 if (first) {
 #pragma unroll
                     for (int g = 0; g < G; ++g)
-                        m[g] = ptx::warp_max(seen ? t[g] + lv : -INFINITY);
+                        m[g] = ptx::warp_max(seen ? t[g] + lv : -INFINITY) - kQ8Bias;
                 }
                 // (a warp without tokens so far has m = -inf: any token is over)
                 float top = t[0] - m[0];
@@ -862,15 +868,17 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                 bool scale_o = false;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float mx = ptx::warp_max(seen ? t[g] + lv : -INFINITY);
+                    const float mx = ptx::warp_max(seen ? t[g] + lv : -INFINITY) - kQ8Bias;
                     float al = 1.f;
                     if (mx > m[g] + kQ8Grow) {
                         // (from -inf there is nothing to rescale)
                         if (m[g] != -INFINITY) {
-                            al = ptx::ex2(m[g] - mx);
+                            // (the sum may take a factor below the normal numbers)
+                            const float root = ptx::ex2(0.5f * (m[g] - mx));
+                            l[g] = l[g] * root * root;
+                            al = root * root;
                             scale_o = true;
                         }
-                        l[g] *= al;
                         m[g] = mx;
                     }
                     if (lane == 0)
@@ -920,7 +928,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                 const uint32_t pw = base + (uint32_t)(L::p_off + ((k & 1) * 4 + w4) * L::kP +
                                                       (lane >> 3) * 128 + (lane & 7) * 16);
                 float x[2 * ((G + 1) / 2)];
-                const float vsx = seen ? vs : 0.f;
+                const float vsx = seen ? vs * 0x1p-24f : 0.f;     // (2^-kQ8Bias)
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     const float e = ptx::ex2(seen ? t[g] - m[g] : -INFINITY);
@@ -993,7 +1001,7 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                     l[g] += __shfl_xor_sync(kFull, l[g], o);
                 if (lane == 0) {
                     my[w4 * 2 * G + g] = m[g];
-                    my[w4 * 2 * G + G + g] = l[g];
+                    my[w4 * 2 * G + G + g] = l[g] * 0x1p-24f;     // (as the weights)
                 }
             }
             if (SETS > 1 && share > 1) {
@@ -1052,7 +1060,9 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 fi[q] = mi[q] == -INFINITY ? 0.f : ptx::ex2(mi[q] - M);
-                sum += mi[q] == -INFINITY ? 0.f : li[q] * fi[q];
+                // (what V scales far apart leave of an accumulator can vanish
+                // next to another's, its sum cannot)
+                sum += mi[q] == -INFINITY ? 0.f : ptx::times_2_to(li[q], mi[q] - M);
             }
 #pragma unroll
             for (int o = G; o < 32; o <<= 1)
@@ -1219,8 +1229,8 @@ __global__ void __launch_bounds__((Q8Smem<D, G>::kThreads), 1)
                     ml = __ldcg(reinterpret_cast<const float2 *>(piece(c) + at));
                 const float f = ml.x == -INFINITY ? 0.f : ptx::ex2(ml.x - M);
                 wt[c * rows + r] = f;
-                if (f != 0.f)
-                    sum += ml.y * f;
+                if (ml.x != -INFINITY)
+                    sum += ptx::times_2_to(ml.y, ml.x - M);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
@@ -1339,8 +1349,8 @@ __global__ void __launch_bounds__(kQ8MergeThreads) q8_merge_kernel(const Q8Decod
     M = ptx::warp_max(M);
 #pragma unroll
     for (int i = 0; i < (kQ8MaxCtas + 31) / 32; ++i) {
+        sum += ml[i].x == -INFINITY ? 0.f : ptx::times_2_to(ml[i].y, ml[i].x - M);
         ml[i].x = ml[i].x == -INFINITY ? 0.f : ptx::ex2(ml[i].x - M);
-        sum += ml[i].x == 0.f ? 0.f : ml[i].y * ml[i].x;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)

@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                    qready = qfull + 8, drain = qready + 8, settled = drain + 16;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen + L::flag_off);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen + L::flag_off + 4);
+    volatile int *tall_flag = reinterpret_cast<volatile int *>(gen + L::flag_off + 8);
 
     const int rank = blockIdx.x % p.split;               // within the cluster
     const int qb = p.qblocks - 1 - (int)(blockIdx.x / p.split % p.qblocks);
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                                                               : 1);
     } else if (tid == 32 * kQpWarpPV) {
         *abort_flag = 0;
+        *tall_flag = 0;
     }
     ptx::fence_mbar_init();
     ptx::grid_wait_prerequisites();
@@ -312,6 +314,8 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             if (!is_k && lane < kQpBoxes) {
                 scales[s * 2 * kQpBoxes + lane] = ks;
                 scales[s * 2 * kQpBoxes + kQpBoxes + lane] = vs;
+                if (vs > 0x1p32f)
+                    *tall_flag = 1;
             }
             __syncwarp();
             if (lane == 0)
@@ -529,7 +533,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             wait(settled + 8u * (4 * (i & 1) + w4), (uint32_t)((i >> 1) & 1));
             const float m = rows_s[r];
             if (m != m_ref && m_ref != -INFINITY)
-                l *= ptx::ex2(m_ref - m);
+                l = ptx::times_2_to(l, m_ref - m);
             m_ref = m;
         };
         for (int i = set; i < ntiles && !fail; i += kQpSets) {
@@ -543,7 +547,10 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             const int tstart = (first + i) * kQpTile;
             const uint32_t sa = s_tm + lane_tm + (uint32_t)((i & 1) * 64);
             float sv[kQpTile], kf[kQpBoxes], lv[kQpBoxes], cand = -INFINITY;
-            bool scaled = true;                          // V scales that have a logarithm
+            // V scales that have a logarithm, none so far above 2^32: past that x =
+            // 2^(s - m + lv) of a small one may be no normal number, while its row
+            // sum x / vs still counts, and the sums are taken of 2^(s - m) itself
+            bool scaled = *tall_flag == 0;
             {
                 uint32_t u0[16], u1[16], u2[16], u3[16];
                 ptx::tmem_ld16(sa, u0);
@@ -602,9 +609,12 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             const bool move = __any_sync(kFull, cand > m_ref + kQpGrow);
             float alpha = 1.f;
             if (move && cand - kQpLift > m_ref) {
-                if (m_ref != -INFINITY)
-                    alpha = ptx::ex2(m_ref - (cand - kQpLift));   // (else nothing to rescale)
-                l *= alpha;
+                const float by = m_ref - (cand - kQpLift);
+                if (m_ref != -INFINITY) {                // (else nothing to rescale)
+                    const float root = ptx::ex2(0.5f * by);   // (l may take less than 2^-126)
+                    l = l * root * root;
+                    alpha = root * root;
+                }
                 m_ref = cand - kQpLift;
             }
             rows_s[r] = m_ref;
@@ -633,7 +643,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     const float vw = scales[vsn * 2 * kQpBoxes + kQpBoxes + x];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float y = ptx::ex2(fmaf(v[e], kf[x], nref));
+                        const float y = ptx::ex2_subnormal(fmaf(v[e], kf[x], nref));
                         l += y;
                         v[e] = y * vw;
                     }
@@ -847,7 +857,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             if (m == -INFINITY && ls == 0.f)
                 continue;                                // no token of this part is seen
             const float f = ptx::ex2(m - M);
-            sum += ls * f;
+            sum += ptx::times_2_to(ls, m - M);
             const uint32_t row = ptx::map_cluster(acc_a + (uint32_t)(r * D * 4), c);
 #pragma unroll
             for (int k = 0; k < D / 128; ++k) {
