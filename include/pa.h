@@ -55,8 +55,9 @@
  *     one on these pools (whose rows are not the last any more).  Kernels
  *     that do not allow an early start (other libraries', most of this one's)
  *     and host copies need no care: the dependent launch behind them happens
- *     when all their blocks have ended, which these two reads rely on.  The
- *     decode over a block-scaled cache reads nothing early.
+ *     when all their blocks have ended, and the early reads rely on that
+ *     alone for what they wrote.  The decode over a block-scaled cache reads
+ *     nothing early.
  */
 #ifndef PA_H_
 #define PA_H_
@@ -230,7 +231,9 @@ pa_status pa_splitk_reduce(void *out, const float *tmp_out, const float *max_log
  * wait inside the kernel that runs out sets PA_DEV_WAIT_TIMEOUT.
  * Arithmetic: scores and the softmax in fp32; the softmax weights are
  * rounded to bf16 for the P.V product (their fp32 values make the row sum);
- * P.V accumulates in fp32; the output is rounded to bf16.
+ * P.V accumulates in fp32; the output is rounded to bf16.  A cached value (V)
+ * that is no number gives NaN in its column for rows of the chunk shortly
+ * before its token too: their weight for it is 0, and 0 times it is NaN.
  */
 pa_status pa_prefill_attention(void *out, const void *query, const int32_t *cu_q_lens, int total_q,
                                int max_q_len, const void *k_pool, const void *v_pool,
@@ -523,7 +526,8 @@ pa_status pa_decode_attention_q8(void *out, const void *query, const void *k_poo
  * and v_scales as in pa_decode_attention_q8.  Arithmetic as there, except that a
  * weight (with its block's V scale) is carried in two parts, E4M3 and the rest
  * as E5M2: off by at most 2^-7 of itself and the lesser of 2^-18 of its row's
- * largest and 2^-3 of itself; one below 2^-22 of the largest may be lost.
+ * largest and 2^-3 of itself; one below 2^-22 of the largest may be lost.  (NaN
+ * among the values of a chunk's own tokens: as there.)
  */
 pa_status pa_prefill_attention_q8(void *out, const void *query, const int32_t *cu_q_lens,
                                   int total_q, int max_q_len, const void *k_pool,

@@ -165,14 +165,6 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 
-// 2^x, hardware approximation, results below 2^-126 kept (subnormal).
-__device__ __forceinline__ float ex2_subnormal(float x)
-{
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // x 2^d, also where 2^d alone is below the normal numbers (d down to -250).
 __device__ __forceinline__ float times_2_to(float x, float d)
 {

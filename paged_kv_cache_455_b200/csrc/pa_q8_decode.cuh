@@ -46,9 +46,11 @@
 //
 // Memory bounds it, behind the ends: setting up, the queries and the first tiles
 // take ~5 us of a call, a segment's end ~2 us, a merge ~3 us.  Measured: 64
-// sequences of up to 4K tokens, 16 query and 4 KV heads of 256, 267 MB: 53.4 us, 5.0
-// TB/s; 8 of 8K, 134 MB: 32.3 us, 4.2 TB/s; 45 of up to 6K, 64 query and 8 KV heads of
-// 128, 239 MB: 59.0 us, 4.1 TB/s; one of 100 tokens: 12.1 us.
+// sequences of up to 4K tokens, 16 query and 4 KV heads of 256, 267 MB: 52.6 us, 5.1
+// TB/s; 8 of 8K, 134 MB: 33.9 us, 4.0 TB/s; 45 of up to 6K, 64 query and 8 KV heads of
+// 128, 239 MB: 58.7 us, 4.1 TB/s.  One sequence, the same heads of 256: without a
+// token 3.2 us, one tile 8.7, 100 tokens 12.3 (four tiles on as many CTAs, joined;
+// 11.4 on one).
 //
 // Work is split as in decode_kernel: every CTA owns a contiguous range of the
 // batch's tiles (mode 0), or whole segments (mode 1); a segment is the run of

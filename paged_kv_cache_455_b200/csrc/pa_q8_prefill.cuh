@@ -34,15 +34,18 @@
 // and lo, 16 columns each, four values per column), O [192, 192 + d), Q hi
 // (d / 4).  Q lo stays in shared memory, where the bf16 queries were: of all
 // operands it costs least there.  Cycles of the products alone, per tile at
-// d = 256: all in tensor memory 1025 (no room for it), Q lo in shared memory 1126,
-// the weights in shared memory 1347.
+// d = 256: all in tensor memory 1025 (no room for it; d = 128 has some, unused),
+// Q lo in shared memory 1126, the weights in shared memory 1347.
 //
 // What bounds it: the tensor cores' 1126 cycles a tile, and around them the
 // softmax warps (528 cycles a tile of exponentials on each scheduler, as much of
 // conversions beside them) and the rescales, for which the product of the
 // tile waits for that of the tile before.  Measured: 16 sequences' chunks of 512
-// tokens over 1-4K, 16 query and 4 KV heads of 256, 352 us (1.05 PFLOP/s counted
-// once, 2.1 of E4M3 products); a bf16 kernel at cuBLAS's rate would take 226 us.
+// tokens over 1-4K, 16 query and 4 KV heads of 256, 340 us (1.09 PFLOP/s counted
+// once, 2.2 of 8-bit products); a bf16 kernel at cuBLAS's rate would take 226 us.
+// 32 query and 8 KV heads of 128: 600 us, floor 243.  The code of a tile should
+// stay small: with a second set of exponentials behind a branch that no tile took
+// the first case took 384 us.
 // A CTA's start and end (Q converted, the first tiles, the last products, the
 // output) take ~8 us besides, hidden by nothing: one CTA fills an SM's tensor
 // memory.
@@ -84,8 +87,8 @@ constexpr int kQpWarpS = 4 * kQpSets, kQpWarpK = kQpWarpS + 1, kQpWarpV = kQpWar
 // largest one for which it gets no new one (E4M3 ends at 448 = 2^8.8).  The
 // lower, the rarer the moves, and the fewer bits small weights keep: with 0 and
 // 8 a tail of 2^-17 beside a weight of 1 loses a tenth of itself.  5 drafted
-// tokens of 32 sequences of 500-4000, 4 heads of 256: 60.5 us, 56.0 with 0 and
-// 8, 61.5 with 5 and 8; prompts of 1024, 145.7 us, 136.4 and 147.3.
+// tokens of 32 sequences of 500-4000, 4 heads of 256: 55.9 us, 54.0 with 0 and
+// 8, 56.1 with 5 and 8; 8 prompts of 1024, 132.8 us, 127.5 and 134.3.
 constexpr float kQpLift = 5.f, kQpGrow = 8.75f;
 
 template <int D>
@@ -547,10 +550,10 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             const int tstart = (first + i) * kQpTile;
             const uint32_t sa = s_tm + lane_tm + (uint32_t)((i & 1) * 64);
             float sv[kQpTile], kf[kQpBoxes], lv[kQpBoxes], cand = -INFINITY;
-            // V scales that have a logarithm, none so far above 2^32: past that x =
-            // 2^(s - m + lv) of a small one may be no normal number, while its row
-            // sum x / vs still counts, and the sums are taken of 2^(s - m) itself
-            bool scaled = *tall_flag == 0;
+            // Once a V scale above 2^32 has been met, x = 2^(s - m + lv) of a small
+            // one may be no normal number, while its row sum x / vs still counts:
+            // then x is carried 2^96 times as large until the sum has been taken.
+            const float bias = *tall_flag == 0 ? 0.f : 96.f;
             {
                 uint32_t u0[16], u1[16], u2[16], u3[16];
                 ptx::tmem_ld16(sa, u0);
@@ -563,7 +566,6 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     const float vw = scales[vsn * 2 * kQpBoxes + kQpBoxes + x];
                     kf[x] = f == 0.f ? 1.2e-38f : f;     // (a masked -inf stays one)
                     lv[x] = fmaxf(ptx::lg2(vw), -64.f);
-                    scaled &= vw >= 5.5e-20f && vw < INFINITY;   // 2^-64: as lv says
                 }
                 ptx::tmem_wait_ld();
                 // S may be overwritten
@@ -628,25 +630,23 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             for (int x = 0; x < kQpBoxes; ++x) {         // 16 tokens at a time
                 float *v = sv + 16 * x;
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                if (scaled) {
-                    const float2 k2 = make_float2(kf[x], kf[x]);
-                    const float2 n2 = make_float2(nref + lv[x], nref + lv[x]);
+                const float2 k2 = make_float2(kf[x], kf[x]);
+                const float n = nref + (lv[x] + bias);
+                const float2 n2 = make_float2(n, n);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float2 y = ptx::fma2(make_float2(v[e], v[e + 1]), k2, n2);
-                        v[e] = ptx::ex2(y.x);
-                        v[e + 1] = ptx::ex2(y.y);
-                        sum[e >> 1 & 1] = ptx::add2(sum[e >> 1 & 1], make_float2(v[e], v[e + 1]));
-                    }
-                    l = fmaf((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), ptx::ex2(-lv[x]), l);
-                } else {
-                    const float vw = scales[vsn * 2 * kQpBoxes + kQpBoxes + x];
+                for (int e = 0; e < 16; e += 2) {
+                    const float2 y = ptx::fma2(make_float2(v[e], v[e + 1]), k2, n2);
+                    v[e] = ptx::ex2(y.x);
+                    v[e + 1] = ptx::ex2(y.y);
+                    sum[e >> 1 & 1] = ptx::add2(sum[e >> 1 & 1], make_float2(v[e], v[e + 1]));
+                }
+                // (in two half steps: the factor may be below the normal numbers)
+                const float root = ptx::ex2(-0.5f * (lv[x] + bias));
+                l = fmaf(((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * root, root, l);
+                if (bias != 0.f) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float y = ptx::ex2_subnormal(fmaf(v[e], kf[x], nref));
-                        l += y;
-                        v[e] = y * vw;
-                    }
+                    for (int e = 0; e < 16; ++e)
+                        v[e] *= 0x1p-96f;
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {

@@ -12,12 +12,15 @@
 //
 // All three kernels only move data: HBM bounds them for prompts, launch and load
 // latency for single tokens.  Measured, 16 query and 4 KV heads of 256, bf16:
-//   pa_rope_and_cache     prompts, 487 MB read and written: 76 us, 6.4 TB/s (0.98
-//                         of a plain copy's rate); 64 single tokens 2.1 us
-//   pa_rope_and_cache_q8  8K tokens in chunks of up to 512, 205 MB: 42 us, 4.8 TB/s;
-//                         256 single tokens 8.5 us with a copy of the lengths
-//   pa_copy_blocks_q8     3000 blocks of 32 tokens, 8 heads of 128, 394 MB: 59.5 us,
-//                         6.6 TB/s; 48 blocks of 16 tokens 2.3 us
+//   pa_rope_and_cache     prompts, 487 MB read and written: 77 us, 6.3 TB/s (0.97
+//                         of a plain copy's rate), 537 MB interleaved 85 us, 430 MB
+//                         of fp32 67 us; 64 single tokens 2.3 us
+//   pa_rope_and_cache_q8  8K tokens in chunks of up to 512, 205 MB: 40.5 us, 5.1 TB/s;
+//                         256 single tokens 6.8 us
+//   pa_copy_blocks_q8     3000 blocks of 32 tokens, 8 heads of 128, 394 MB: 60.3 us,
+//                         6.5 TB/s; 48 blocks of 16 tokens 2.5 us; 512 blocks to pinned
+//                         host memory and back 52 and 51 GB/s (one copy of as many
+//                         bytes: 55)
 // What keeps the second from the copy's rate is its chain of loads (a CTA of the
 // cache part finds its sequence, then its block, and only then writes) and its
 // arithmetic: the schedulers issue half of the time.  64 registers a thread for
@@ -813,9 +816,9 @@ pa_status pa_rope_and_cache_q8_strided(
     // nothing to do for the queries when they are not rotated in place
     const bool rotate_q = num_q_heads > 0 && !(rot_dim == 0 && query == query_out);
     // Four rows a thread once they fill the GPU several times over, one for the
-    // few rows of single tokens: 8K new tokens of 16 query heads of 256 take
+    // few rows of single tokens: 8K new tokens of 16 query heads of 256 took
     // 45 us with four and 49 us with two one after the other, 256 tokens 9.6 us
-    // with four and 8.5 us with one.
+    // with four and 8.5 us with one (these with a copy of the lengths).
     const int64_t query_ctas = (int64_t)total_q * num_q_heads / (128 / (head_dim / 16));
     p.query_rows = query_ctas >= 148 * 16 * 4 ? kQ8QueryRows : 1;
     const int rows_per_cta = 128 / (head_dim / 16) * p.query_rows;
